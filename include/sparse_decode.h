@@ -347,6 +347,105 @@ sparse_status_t sparse_louver_decode_step(const sparse_shape_t *shape, int32_t L
                                           float *lse, void *louver_ws, size_t louver_ws_bytes,
                                           void *ws, size_t ws_bytes, void *stream);
 
+/* ---- Paged caches ----------------------------------------------------------
+ * The serving side of the decode step: ragged batches whose caches grow in
+ * pages, the rows of new tokens written into them, and the attention of those
+ * tokens over everything cached so far (a prompt's chunk, or one token each),
+ * optionally under a sliding window with a few first tokens that stay visible
+ * (CLSA article, section CLSAの仕組み: the self-decoder below the shared cache
+ * is such an attention, and generates the cache the decode step routes over).
+ *
+ *   K, V  [num_pages, Hkv, page_size, d]: a page holds page_size consecutive
+ *         tokens of one sequence, head by head.  A dense cache [B,Hkv,n_cap,d]
+ *         is the paged cache of B pages of n_cap tokens whose table is
+ *         block_table[b][0] = b, so these calls fill and read the caches of
+ *         the decode step too.
+ *   block_table [B, max_blocks] int32: sequence b's token j is in page
+ *         block_table[b][j / page_size], row j % page_size.  Entries past a
+ *         sequence's length, or of tokens that no new token sees, are not
+ *         read and may hold anything.
+ *   New tokens are packed, all sequences one after another: sequence b owns
+ *         rows q_start[b] .. q_start[b+1] - 1 of the T rows of q, k_new,
+ *         v_new and out; rows from q_start[B] on are padding.
+ * q, k_new and v_new may be column ranges of wider rows: their strides are the
+ * elements between two tokens' rows, a multiple of 16 bytes.
+ *
+ * page_size is a multiple of 16, or max_blocks is 1; B <= 4096; T <= 2^24;
+ * num_pages * page_size < 2^31; max_blocks * page_size <= 2^30; d, dtype and
+ * Hq / Hkv as everywhere. */
+typedef struct {
+  int32_t B;          /* sequences */
+  int32_t T;          /* rows of the packed tensors: at least the new tokens */
+  int32_t Hq;         /* query heads */
+  int32_t Hkv;        /* KV heads; Hq % Hkv == 0 */
+  int32_t d;          /* head dimension */
+  int32_t dtype;      /* sparse_dtype_t of q, K, V, k_new, v_new and out */
+  int32_t page_size;  /* tokens per page */
+  int32_t num_pages;  /* pages in K and in V */
+  int32_t max_blocks; /* columns of the block table */
+  int32_t max_new;    /* most new tokens that one sequence has (0: T) */
+} sparse_paged_shape_t;
+
+/* Bytes of workspace that sparse_paged_attn needs for this shape (the other
+ * paged calls need 4096).  A workspace may also serve the entry points above
+ * for shapes of B * Hkv <= 256, the calls being ordered.  Synchronous. */
+sparse_status_t sparse_paged_workspace_size(const sparse_paged_shape_t *shape, size_t *bytes);
+
+/* The block tables and slot map of one batch step, from the requests'
+ * lengths: sequence b has lens[b] cached tokens and gets new_lens[b] more
+ * (0 allowed).  Pages it lacks are taken from the end of the free list
+ * (free_pages[0 .. *free_count), capacity free_cap), sequences in order, a
+ * sequence's blocks in order, and entered in its row of block_table.
+ *   kv_lens [B] = lens + new_lens;  q_start [B+1]: rows of the new tokens;
+ *   positions [T]: a row's position in its sequence;  slots [T]: page *
+ *   page_size + row of the page;  both -1 for padding rows;
+ *   free_left [1] = what remains of the free list.
+ * kv_lens may be lens and free_left may be free_count (updated in place);
+ * otherwise the call repeats with the same results.  A batch that does not
+ * fit -- more new tokens than T, more pages than are free, a sequence longer
+ * than its table row -- is refused as a whole (SPARSE_ERR_CAPACITY in the
+ * device status; lengths that are negative or a free count outside
+ * [0, free_cap]: SPARSE_ERR_INDEX): no page is taken, q_start is 0, positions
+ * and slots are -1, kv_lens = lens.  A free or already entered page id outside
+ * [0, num_pages) raises SPARSE_ERR_INDEX and gives slot -1.  Pages of a
+ * finished request return to the list by writing them behind its end.
+ * Hq, Hkv, d, dtype are only checked. */
+sparse_status_t sparse_paged_plan(const sparse_paged_shape_t *shape, const int32_t *new_lens,
+                                  const int32_t *lens, int32_t *block_table,
+                                  const int32_t *free_pages, int32_t free_cap,
+                                  const int32_t *free_count, int32_t *kv_lens, int32_t *q_start,
+                                  int32_t *positions, int32_t *slots, int32_t *free_left, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/* The new tokens' rows into their pages: row t of k_new and v_new (T rows of
+ * [Hkv,d], k_stride and v_stride elements apart) becomes row slots[t] %
+ * page_size of page slots[t] / page_size in K and V, for every head.  Rows
+ * with slot -1 are skipped; other slots outside the pool are skipped and
+ * raise SPARSE_ERR_INDEX in the device status.  Slots are distinct. */
+sparse_status_t sparse_paged_append(const sparse_paged_shape_t *shape, void *K, void *V,
+                                    const void *k_new, int64_t k_stride, const void *v_new,
+                                    int64_t v_stride, const int32_t *slots, void *ws,
+                                    size_t ws_bytes, void *stream);
+
+/* Attention of the new tokens over their sequences' caches, themselves
+ * included: row i of sequence b stands at position p = kv_lens[b] -
+ * (q_start[b+1] - q_start[b]) + i and sees tokens j <= p; with window >= 1
+ * only those with j > p - window or j < sinks.  out [T,Hq,d], lse [T,Hq] or
+ * NULL, as in sparse_attn_gather (nothing seen: o = 0, lse = -inf); padding
+ * rows are left as they were.  K and V already hold the new tokens' rows.
+ * A page id outside [0, num_pages) hides its tokens and raises
+ * SPARSE_ERR_INDEX; a sequence with lengths outside the shape (rows outside
+ * [0,T], more than max_new new tokens, a negative kv_len or one beyond its
+ * table row) is skipped and raises it too.  Rows of K and V that no new token
+ * of the sequence sees are never used, whatever they hold; one that some new
+ * tokens see must be finite (a value times a weight of zero reaches the
+ * tokens near them that do not see it). */
+sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void *q,
+                                  int64_t q_stride, const void *K, const void *V,
+                                  const int32_t *block_table, const int32_t *q_start,
+                                  const int32_t *kv_lens, int32_t window, int32_t sinks, void *out,
+                                  float *lse, void *ws, size_t ws_bytes, void *stream);
+
 /* Self-test of failure detection, with no fault: one device thread waits,
  * through the bounded wait that every counter barrier of the library uses
  * (the Louver query's per-head barrier), on a workspace word that nothing

@@ -29,7 +29,8 @@ __all__ = ["SparseDecodeError", "lib_path", "load", "score", "select_topk",
            "Workspace", "STATUS_NAMES", "EXPORTED_SYMBOLS", "decode_step_grouped",
            "kv_append", "LouverIndex", "louver_build", "louver_route_threshold",
            "DecodeStepGraph", "selftest_bounded_wait", "louver_decode_step",
-           "device_usable", "read_device_flags", "FLAG_SLOW_SELECT"]
+           "device_usable", "read_device_flags", "FLAG_SLOW_SELECT",
+           "paged_plan", "paged_append", "paged_attn", "paged_workspace_bytes"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_FILE = os.path.join(_PKG, "libsparse_decode.so")
@@ -50,7 +51,8 @@ EXPORTED_SYMBOLS = (
     "sparse_louver_sizes", "sparse_louver_build", "sparse_louver_route_threshold",
     "sparse_selftest_bounded_wait", "sparse_louver_decode_step",
     "sparse_pointer_device_usable", "sparse_graph_launch", "sparse_decode_step_join",
-    "sparse_decode_step_fused", "sparse_graph_upload",
+    "sparse_decode_step_fused", "sparse_graph_upload", "sparse_paged_workspace_size",
+    "sparse_paged_plan", "sparse_paged_append", "sparse_paged_attn",
 )
 
 DTYPE_CODES = {torch.float32: 0, torch.bfloat16: 1}
@@ -89,6 +91,7 @@ def load():
                 "(run `python -m token_sparse_attention_sm_b200.build`)")
         lib = ctypes.CDLL(_LIB_FILE)
         P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        I64 = ctypes.c_int64
         SH = ctypes.POINTER(_Shape)
         sigs = {
             "sparse_status_string": (ctypes.c_char_p, [I32]),
@@ -122,6 +125,10 @@ def load():
             "sparse_pointer_device_usable": (I32, [P, ctypes.POINTER(I32)]),
             "sparse_graph_launch": (I32, [P, P]),
             "sparse_graph_upload": (I32, [P, P]),
+            "sparse_paged_workspace_size": (I32, [P, ctypes.POINTER(SZ)]),
+            "sparse_paged_plan": (I32, [P, P, P, P, P, I32, P, P, P, P, P, P, P, SZ, P]),
+            "sparse_paged_append": (I32, [P, P, P, P, I64, P, I64, P, P, SZ, P]),
+            "sparse_paged_attn": (I32, [P, P, I64, P, P, P, P, P, I32, I32, P, P, P, SZ, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -960,3 +967,5 @@ def louver_decode_step(q_route, q_layers, K, V, index: LouverIndex, tau, cap: in
         read_device_status(w)
     return {"idx": idx, "count": count, "out": out, "lse": lse}
 
+
+from .paged import paged_append, paged_attn, paged_plan, paged_workspace_bytes  # noqa: E402

@@ -1,0 +1,106 @@
+// paged.cuh -- what the kernels over a paged K/V cache share: the arguments,
+// which keys a block of query rows sees, and the schedule of a call (how the
+// rows of a ragged batch are cut into work items), which one small kernel
+// derives on the device from the sequences' lengths.
+//
+// A new token i of sequence b stands at position p = kv_len[b] - n[b] + i and
+// sees key j when 0 <= j <= p and, under a window w, j > p - w or j < sinks.
+// Query rows of one KV head are (token, query head of the group) pairs,
+// token-major: row r of a block of TB tokens is token r / G, head r % G, so
+// the G heads that share a KV head share every key tile read.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace sd {
+
+// One sequence's part of the schedule, written by the schedule kernel.
+struct PgSeq {
+  int base;  // work items (per KV head) before this sequence
+  int slot;  // partial slots (per KV head) before this sequence
+  int np;    // pieces its key range is cut into (1: no partials)
+  int len;   // key tiles per piece
+};
+// The schedule in the workspace: header, then PgSeq[B + 1] (the last one
+// holds the totals).
+struct PgHead {
+  uint32_t next;  // claim counter of the work items
+  uint32_t pad[15];
+};
+
+struct PgArgs {
+  const void *q, *K, *V;
+  const int *table, *q_start, *kv_lens;
+  void *out;
+  float *lse;
+  long long q_stride;  // elements between the tokens of q
+  int B, T, Hq, Hkv, page, pages, blocks, window, sinks, max_new;
+  float scale_log2;
+  uint32_t *status;
+  // schedule and partials (workspace)
+  PgHead *head;
+  PgSeq *seqs;
+  uint32_t *arrive;  // [slot_cap * Hkv], zeroed by the schedule kernel
+  float *part;       // [slot_cap * Hkv][part_rows][d] then [..][part_rows] (max, sum)
+  int slot_cap;      // partial slots per KV head
+  int part_rows;
+};
+
+// The key tiles a block of tokens [t0, t1) of a sequence reads: tiles
+// [0, sink_tiles) and [lo, hi), KT keys each.
+struct PgTiles {
+  int sink_tiles, lo, hi;
+  __device__ int units() const { return sink_tiles + hi - lo; }
+  __device__ int tile(int u) const { return u < sink_tiles ? u : u - sink_tiles + lo; }
+};
+
+// The first key that the window leaves a row at position p (0: no window).
+__device__ __forceinline__ int pg_window_low(int p, int window) {
+  const long long lo = (long long)p - window + 1;
+  return window > 0 && lo > 0 ? (int)lo : 0;
+}
+
+__device__ __forceinline__ PgTiles pg_tiles(int p_first, int p_last, int window, int sinks,
+                                            int KT) {
+  PgTiles t;
+  const int hi = max(p_last + 1, 0);
+  const int lo = pg_window_low(p_first, window);
+  t.hi = (hi + KT - 1) / KT;
+  t.lo = min(lo / KT, t.hi);
+  t.sink_tiles = min((min(sinks, hi) + KT - 1) / KT, t.lo);
+  return t;
+}
+
+// A sequence's lengths as given, or false if they make no sense (the schedule
+// kernel reports that).
+__device__ __forceinline__ bool pg_lengths(const PgArgs &a, int b, int *row0, int *n, int *kv) {
+  const int s = a.q_start[b], e = a.q_start[b + 1], c = a.kv_lens[b];
+  *row0 = s;
+  *n = e - s;
+  *kv = c;
+  return s >= 0 && e >= s && e <= a.T && c >= 0 && e - s <= a.max_new &&
+         (long long)c <= (long long)a.blocks * a.page;
+}
+
+// The sequence (and its schedule entry) that work item x of a head is in:
+// the last one with base <= x.  One warp, 32 probes a round.
+__device__ __forceinline__ int pg_find(const PgSeq *seqs, int B, int x, PgSeq *out) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;  // seqs[lo].base <= x < seqs[lo + n].base
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = min(lo + lane * step, lo + n);
+    const bool le = seqs[at].base <= x && at < lo + n;
+    const uint32_t m = __ballot_sync(0xffffffffu, le);
+    const int k = __popc(m) - 1;
+    const int nlo = lo + k * step;
+    n = min(step, lo + n - nlo);
+    lo = nlo;
+  }
+  *out = seqs[lo];
+  return lo;
+}
+
+}  // namespace sd

@@ -1,0 +1,32 @@
+// paged.h -- host side of the paged-cache operators, shared between their
+// translation units.
+#pragma once
+
+#include "internal.h"
+
+namespace sd {
+
+struct PgArgs;
+
+// A caller's paged shape after the checks every entry point shares.
+struct PagedShape {
+  int B, T, Hq, Hkv, d, dtype, page, pages, blocks, max_new;
+  int G() const { return Hq / Hkv; }
+  int esize() const { return dtype == 0 ? 4 : 2; }
+};
+constexpr int kPagedMaxB = 4096;  // sequences a call may have
+
+// Workspace of the attention: the schedule, then the partials.
+struct PagedLayout {
+  size_t head_off, seqs_off, arrive_off, part_off, total;
+  int slot_cap, part_rows;
+};
+
+// fp32 inputs (paged_attn.cu): CUDA cores.
+cudaError_t launch_paged_attn_simt(const PagedShape &s, const PgArgs &a, cudaStream_t st);
+// The work items' schedule for row blocks of `tb` tokens, key tiles of `kt`
+// keys and `grid` workers (paged_sched.cu).
+cudaError_t launch_paged_schedule(const PagedShape &s, const PgArgs &a, int tb, int kt, int grid,
+                                  cudaStream_t st);
+
+}  // namespace sd

@@ -1,0 +1,349 @@
+// paged_attn.cu -- attention of new tokens over a paged cache on the CUDA
+// cores: o_i = sum_j softmax(z_i)_j v_j, z_ij = <q_i, k_j> / sqrt(d) over the
+// keys row i sees, one pass over the keys with a running maximum m and sum l
+// (when a tile raises m, o and l are scaled by exp2(m_old - m_new)).
+//
+// A worker (CTA) claims items of the schedule: a block of RB query rows of
+// one (sequence, KV head) and a piece of its key tiles.  Each tile of 64 keys
+// is copied into shared memory as fp32, K for S = Q K^T and V for O += P V
+// in turn, the next tile's K arriving while V is used and the other way round.
+// Thread (ty, tx) holds rows ty*4 .. +3 and keys tx + TX*j of S, then columns
+// of O; a row's TX threads are in one warp, so its maximum and sum are warp
+// shuffles.  A piece of a cut range writes (O, m, l) to its slot; the last
+// piece of the block to arrive merges them in piece order.
+#include "paged.h"
+#include "paged.cuh"
+
+namespace sd {
+namespace {
+
+constexpr int kKT = 64;  // keys per tile
+
+template <int D, int RB>
+struct SimtCfg {
+  static constexpr int TX = RB == 16 ? 32 : 16;
+  static constexpr int kThreads = RB / 4 * TX;
+  static constexpr int NK = kKT / TX;      // keys per thread
+  static constexpr int NC = D / TX;        // columns per thread
+  static constexpr int QS = D + 4;         // row strides, in floats
+  static constexpr int KS = D + 4;
+  static constexpr int PS = kKT + 4;
+  static constexpr int kFloats = RB * QS + 2 * kKT * KS + RB * PS;
+  static constexpr int kSmem = kFloats * 4 + 64 + kKT;  // + the claimed item, key flags
+  static constexpr int VEC = NC >= 4 ? 4 : NC;  // columns of V read at once
+};
+
+__device__ __forceinline__ void cp16(void *dst, const void *src, bool pred) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(pred ? 16u : 0u)
+               : "memory");
+}
+
+// keys [key0, key0 + 64) of the sequence, those in [0, limit) that any row of
+// the block sees (j >= low or j < sinks), into dst as fp32 rows; zeros for
+// the others and for pages outside the pool.  kok (nullable): which were read.
+template <typename T, int D, int KS, int THREADS>
+__device__ __forceinline__ void load_tile(float *dst, unsigned char *kok, const T *cache,
+                                          const PgArgs &a, const int *table, int h, int key0,
+                                          int limit, int low) {
+  constexpr int PER = 16 / sizeof(T);  // elements of a 16-byte piece
+  constexpr int CPR = D / PER;
+  for (int p = threadIdx.x; p < kKT * CPR; p += THREADS) {
+    const int r = p / CPR, c = p % CPR;
+    const int j = key0 + r;
+    bool ok = j < limit && (j >= low || j < a.sinks);
+    size_t off = 0;
+    if (ok) {
+      const int pg = table[j / a.page];
+      ok = pg >= 0 && pg < a.pages;
+      if (ok) off = (((size_t)pg * a.Hkv + h) * a.page + j % a.page) * D + c * PER;
+      else if (c == 0) raise_flag(a.status, FLAG_INDEX);
+    }
+    if (kok && c == 0) kok[r] = ok;
+    if constexpr (sizeof(T) == 4) {
+      cp16(dst + r * KS + c * PER, cache + off, ok);
+    } else {
+      float f[PER];
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (ok) v = *reinterpret_cast<const uint4 *>(cache + off);
+      unpack16<T>(v, f);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) dst[r * KS + c * PER + i] = f[i];
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <typename T, int D, int RB>
+__global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kernel(const PgArgs a) {
+  using C = SimtCfg<D, RB>;
+  constexpr int TX = C::TX, NK = C::NK, NC = C::NC, QS = C::QS, KS = C::KS, PS = C::PS;
+  constexpr int THREADS = C::kThreads;
+  extern __shared__ float sm[];
+  float *Qs = sm, *Ks = Qs + RB * QS, *Vs = Ks + kKT * KS, *Ps = Vs + kKT * KS;
+  int *box = reinterpret_cast<int *>(Ps + RB * PS);
+  unsigned char *kok = reinterpret_cast<unsigned char *>(box + 16);
+  const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
+  const int G = a.Hq / a.Hkv, TB = RB / G;
+  const T *q = static_cast<const T *>(a.q), *K = static_cast<const T *>(a.K),
+          *V = static_cast<const T *>(a.V);
+  T *out = static_cast<T *>(a.out);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int per_head = a.seqs[a.B].base;
+
+  for (;;) {
+    if (tid == 0) box[0] = (int)min(atomicAdd(&a.head->next, 1u), 0x7fffffffu);
+    __syncthreads();
+    const long long item = box[0];
+    __syncthreads();
+    if (item >= (long long)per_head * a.Hkv) break;
+    const int h = (int)(item / per_head), x = (int)(item % per_head);
+    PgSeq sq;
+    const int b = pg_find(a.seqs, a.B, x, &sq);
+    int row0, n, kv;
+    pg_lengths(a, b, &row0, &n, &kv);
+    const int nrb = (n + TB - 1) / TB;
+    // piece-major, the longest ranges first
+    const int piece = (x - sq.base) / nrb, rb = nrb - 1 - (x - sq.base) % nrb;
+    const int t0 = rb * TB, t1 = min(n, t0 + TB), rows = (t1 - t0) * G;
+    const int p_first = kv - n + t0, p_last = kv - n + t1 - 1;
+    const PgTiles tiles = pg_tiles(p_first, p_last, a.window, a.sinks, kKT);
+    const int u0 = piece * sq.len, u1 = min(tiles.units(), u0 + sq.len);
+    const int limit = p_last + 1, low = pg_window_low(p_first, a.window);
+    const int *table = a.table + (size_t)b * a.blocks;
+
+    for (int p = tid; p < RB * (D / 4); p += THREADS) {
+      const int r = p / (D / 4), c = p % (D / 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows) {
+        const T *src = q + (size_t)(row0 + t0 + r / G) * a.q_stride + (h * G + r % G) * D + c * 4;
+        v = make_float4(DT<T>::to_f(src[0]), DT<T>::to_f(src[1]), DT<T>::to_f(src[2]),
+                        DT<T>::to_f(src[3]));
+      }
+      *reinterpret_cast<float4 *>(Qs + r * QS + c * 4) = v;
+    }
+    float m[4], l[4], o[4][NC];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
+    }
+    int pos[4], lowr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      pos[i] = r < rows ? p_first + r / G : -1;
+      lowr[i] = pg_window_low(pos[i], a.window);
+    }
+    if (u0 < u1)
+      load_tile<T, D, KS, THREADS>(Ks, kok, K, a, table, h, tiles.tile(u0) * kKT, limit, low);
+    for (int u = u0; u < u1; ++u) {
+      const int key0 = tiles.tile(u) * kKT;
+      load_tile<T, D, KS, THREADS>(Vs, nullptr, V, a, table, h, key0, limit, low);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncthreads();
+      float s[4][NK];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NK; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < D; k += 4) {
+        float4 qv[4], kv4[NK];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          qv[i] = *reinterpret_cast<const float4 *>(Qs + (ty * 4 + i) * QS + k);
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+          kv4[j] = *reinterpret_cast<const float4 *>(Ks + (tx + TX * j) * KS + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < NK; ++j) {
+            s[i][j] = fmaf(qv[i].x, kv4[j].x, s[i][j]);
+            s[i][j] = fmaf(qv[i].y, kv4[j].y, s[i][j]);
+            s[i][j] = fmaf(qv[i].z, kv4[j].z, s[i][j]);
+            s[i][j] = fmaf(qv[i].w, kv4[j].w, s[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float mx = m[i];
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+          const int key = key0 + tx + TX * j;
+          const bool see =
+              key <= pos[i] && (key >= lowr[i] || key < a.sinks) && kok[tx + TX * j];
+          s[i][j] = see ? s[i][j] * a.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int w = TX / 2; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        const float use = mx == -INFINITY ? 0.f : mx;
+        const float corr = exp2f(m[i] - use);
+        m[i] = mx;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+          const float p = exp2f(s[i][j] - use);
+          sum += p;
+          Ps[(ty * 4 + i) * PS + tx + TX * j] = p;
+        }
+        l[i] = l[i] * corr + sum;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[i][c] *= corr;
+      }
+      __syncthreads();  // K is used up, P complete
+      if (u + 1 < u1)
+        load_tile<T, D, KS, THREADS>(Ks, kok, K, a, table, h, tiles.tile(u + 1) * kKT, limit, low);
+      else
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncthreads();  // V has landed
+#pragma unroll 2
+      for (int k = 0; k < kKT; k += 4) {
+        float4 pv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          pv[i] = *reinterpret_cast<const float4 *>(Ps + (ty * 4 + i) * PS + k);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          float v[NC];
+#pragma unroll
+          for (int c = 0; c < NC; c += C::VEC) {
+            const float *src = Vs + (k + kk) * KS + (c / C::VEC) * (TX * C::VEC) + tx * C::VEC;
+#pragma unroll
+            for (int e = 0; e < C::VEC; ++e) v[c + e] = src[e];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[i][c] = fmaf(p, v[c], o[i][c]);
+          }
+        }
+      }
+      __syncthreads();  // V and P are used up
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // the row's sum over its threads
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int w = TX / 2; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+
+    if (sq.np == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
+        if (r >= rows) continue;
+        const size_t tok = (size_t)(row0 + t0 + r / G), hq = h * G + r % G;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int col = (c / C::VEC) * (TX * C::VEC) + tx * C::VEC + c % C::VEC;
+          out[(tok * a.Hq + hq) * D + col] = DT<T>::from_f(o[i][c] * inv);
+        }
+        if (a.lse && tx == 0)
+          a.lse[tok * a.Hq + hq] =
+              l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+      }
+    } else {
+      const size_t first = (size_t)(sq.slot + rb * sq.np) * a.Hkv;  // slots (piece, head)
+      const size_t per = (size_t)a.part_rows * D;
+      float2 *ml = reinterpret_cast<float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
+      const size_t mine = first + (size_t)piece * a.Hkv + h;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
+        if (r >= rows) continue;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int col = (c / C::VEC) * (TX * C::VEC) + tx * C::VEC + c % C::VEC;
+          a.part[mine * per + (size_t)r * D + col] = o[i][c];
+        }
+        if (tx == 0) ml[mine * a.part_rows + r] = make_float2(m[i], l[i]);
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) box[0] = atomicAdd(&a.arrive[first + h], 1u) == (uint32_t)(sq.np - 1);
+      __syncthreads();
+      const bool last = box[0] != 0;
+      __syncthreads();
+      if (last) {
+        __threadfence();
+        for (int r = tid / 32; r < rows; r += THREADS / 32) {
+          const int lane = tid & 31;
+          float mm = -INFINITY;
+          for (int p = 0; p < sq.np; ++p)
+            mm = fmaxf(mm, __ldcg(&ml[(first + (size_t)p * a.Hkv + h) * a.part_rows + r].x));
+          const float use = mm == -INFINITY ? 0.f : mm;
+          float acc[D / 32] = {}, ll = 0.f;
+          for (int p = 0; p < sq.np; ++p) {
+            const size_t s = first + (size_t)p * a.Hkv + h;
+            const float2 e = __ldcg(&ml[s * a.part_rows + r]);
+            const float w = exp2f(e.x - use);
+            ll += e.y * w;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+              acc[c] += __ldcg(&a.part[s * per + (size_t)r * D + c * 32 + lane]) * w;
+          }
+          const float inv = ll > 0.f ? 1.f / ll : 0.f;
+          const size_t tok = (size_t)(row0 + t0 + r / G), hq = h * G + r % G;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+            out[(tok * a.Hq + hq) * D + c * 32 + lane] = DT<T>::from_f(acc[c] * inv);
+          if (a.lse && lane == 0)
+            a.lse[tok * a.Hq + hq] =
+                ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int D, int RB>
+cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
+  using C = SimtCfg<D, RB>;
+  auto kern = paged_attn_simt_kernel<T, D, RB>;
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  int per_sm = 1;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, C::kThreads, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int grid = di.sm_count * (per_sm < 1 ? 1 : per_sm);
+  if ((e = launch_paged_schedule(s, a, RB / s.G(), kKT, grid, st)) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attrs[1];
+  cfg.attrs = attrs;
+  cfg.numAttrs = 0;
+  add_pdl_attr(cfg, attrs);
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <typename T, int D>
+cudaError_t pick(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
+  // up to 16 rows per (sequence, KV head): the cache is read once, memory bound
+  return s.max_new * s.G() <= 16 ? run<T, D, 16>(s, a, st) : run<T, D, 64>(s, a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attn_simt(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
+  if (s.dtype == 0) return s.d == 64 ? pick<float, 64>(s, a, st) : pick<float, 128>(s, a, st);
+  return s.d == 64 ? pick<__nv_bfloat16, 64>(s, a, st) : pick<__nv_bfloat16, 128>(s, a, st);
+}
+
+}  // namespace sd

@@ -1,0 +1,257 @@
+"""Paged caches: block tables and slot maps of a ragged batch, the append of
+new rows by slot, and the attention of new tokens over their paged caches
+(CLSA article, section CLSAの仕組み: the self-decoder whose cache the decode
+step routes over is such an attention).
+
+A cache is K, V [num_pages, Hkv, page_size, d]; sequence b's token j is row
+j % page_size of page block_table[b, j // page_size].  A dense cache
+[B,Hkv,n_cap,d] is the paged cache of B pages with block_table[b, 0] = b, so
+these calls also fill and read the caches of ``decode_step``.
+
+A serving step is ``paged_plan`` once, then per layer ``paged_append`` and
+``paged_attn`` with what it returned::
+
+    p = sd.paged_plan(new_lens, lens, table, free_pages, free_count, 64, T, num_pages)
+    sd.paged_append(K, V, k_new, v_new, p["slots"])
+    out, lse = sd.paged_attn(q, K, V, table, p["q_start"], p["kv_lens"])
+    lens, free_count = p["kv_lens"], p["free_left"]
+
+Without ``ws`` a call uses a workspace kept for its device and stream; inside
+a stream capture it takes one from the graph's own memory instead, so two
+captured graphs never share scratch.  Calls given one Workspace are ordered by
+the caller, and a capture needs it to be large enough already.  ``check``
+reads the device status (and synchronises); a capture needs check=False.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import (DTYPE_CODES, Workspace, _check, _need_cuda, _need_result, _ptr, _stream, load,
+               read_device_status)
+
+_HEADER = 4096  # workspace bytes of the calls that only report a status
+_stream_ws: dict = {}
+
+
+class _PagedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "T", "Hq", "Hkv", "d", "dtype", "page_size", "num_pages", "max_blocks",
+                 "max_new")]
+
+
+def _shape(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new=0) -> _PagedShape:
+    if dtype not in DTYPE_CODES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return _PagedShape(B, T, Hq, Hkv, d, DTYPE_CODES[dtype], page_size, num_pages, max_blocks,
+                       max_new)
+
+
+def _one_device(*ts) -> torch.device:
+    """The device all given tensors are on."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and on {t.device}")
+        dev = t.device
+    return dev
+
+
+class _Scratch:
+    """The workspace buffer of one call: its pointer, and the status to read."""
+
+    def __init__(self, ws: Workspace | None, device, nbytes: int, check: bool):
+        capturing = torch.cuda.is_current_stream_capturing()
+        if capturing and check:
+            raise ValueError("check=True synchronises: give check=False inside a stream capture")
+        self.ws = ws
+        if ws is not None:
+            if ws.device.index not in (None, device.index):
+                raise ValueError(f"workspace on {ws.device}, tensors on {device}")
+            if capturing and (ws.buf is None or ws.buf.numel() < nbytes):
+                raise ValueError("a workspace cannot grow inside a stream capture: "
+                                 f"get({nbytes}) before it")
+            self.buf = ws.get(nbytes)
+            if capturing:  # the graph keeps this address, also when ws grows later
+                ws.kept = getattr(ws, "kept", []) + [self.buf]
+        elif capturing:
+            # written before it is read, and never checked: no need to clear it
+            self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        else:
+            key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+            if key not in _stream_ws:
+                _stream_ws[key] = Workspace(device)
+            self.ws = _stream_ws[key]
+            self.buf = self.ws.get(nbytes)
+
+    def args(self):
+        return _ptr(self.buf), self.buf.numel(), _stream()
+
+    def finish(self, check: bool):
+        if check:
+            read_device_status(self.ws)
+
+
+def _rows(t, name: str, heads: int, d: int) -> int:
+    """The elements between the token rows of t [T,heads,d]; its heads and
+    elements must be dense."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [T,{heads},{d}], got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if t.shape[0] < 2:
+        return heads * d
+    if t.stride(0) < heads * d or t.stride(0) * t.element_size() % 16:
+        raise ValueError(f"the rows of {name} must be distinct and a multiple of 16 bytes apart")
+    return t.stride(0)
+
+
+def _need_int32(t, shape, name: str):
+    _need_result(t, shape, torch.int32, name)
+
+
+def _cache_dims(K, V):
+    if K.dim() != 4 or V.shape != K.shape or V.dtype != K.dtype:
+        raise ValueError("K and V must be [num_pages,Hkv,page_size,d] of one shape and dtype")
+    if not (K.is_contiguous() and V.is_contiguous()):
+        raise ValueError("K and V must be contiguous")
+    return K.shape
+
+
+def paged_workspace_bytes(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks,
+                          max_new: int | None = None) -> int:
+    """Bytes that paged_attn needs of a workspace for these sizes."""
+    n = ctypes.c_size_t(0)
+    sh = _shape(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new or 0)
+    _check(load().sparse_paged_workspace_size(ctypes.byref(sh), ctypes.byref(n)),
+           "paged_workspace_size")
+    return int(n.value)
+
+
+def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: int,
+               num_tokens: int, num_pages: int, ws: Workspace | None = None, check: bool = True,
+               kv_lens=None, q_start=None, positions=None, slots=None, free_left=None):
+    """The block tables and slot map of one batch step, on the device from the
+    requests' lengths (sparse_paged_plan).
+
+    new_lens, lens [B] int32: new and already cached tokens of every sequence;
+    block_table [B,max_blocks] int32, updated in place; free_pages [F] int32
+    and free_count [1] int32: the free list, pages taken from its end;
+    num_tokens: rows of the packed tensors (at least the new tokens).  Returns
+    dict(kv_lens [B], q_start [B+1], positions [T], slots [T], free_left [1]),
+    all int32; kv_lens may be lens and free_left free_count to update them in
+    place.  A batch that does not fit raises (SPARSE_ERR_CAPACITY) and takes
+    nothing."""
+    dev = _one_device(new_lens, lens, block_table, free_pages, free_count, kv_lens, q_start,
+                      positions, slots, free_left)
+    if new_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("new_lens must be [B], block_table [B,max_blocks], free_pages [F]")
+    B, T, F = new_lens.shape[0], int(num_tokens), free_pages.shape[0]
+    if T < 0:
+        raise ValueError("num_tokens must not be negative")
+    for t, s, name in [(new_lens, (B,), "new_lens"), (lens, (B,), "lens"),
+                       (block_table, (B, block_table.shape[1]), "block_table"),
+                       (free_pages, (F,), "free_pages"), (free_count, (1,), "free_count"),
+                       (kv_lens, (B,), "kv_lens"), (q_start, (B + 1,), "q_start"),
+                       (positions, (T,), "positions"), (slots, (T,), "slots"),
+                       (free_left, (1,), "free_left")]:
+        _need_int32(t, s, name)
+    sh = _shape(B, T, 1, 1, 64, torch.float32, int(page_size), int(num_pages),
+                block_table.shape[1])
+    with torch.cuda.device(dev):
+        scratch = _Scratch(ws, dev, _HEADER, check)
+        new = {"dtype": torch.int32, "device": dev}
+        kv_lens = torch.empty(B, **new) if kv_lens is None else kv_lens
+        q_start = torch.empty(B + 1, **new) if q_start is None else q_start
+        positions = torch.empty(T, **new) if positions is None else positions
+        slots = torch.empty(T, **new) if slots is None else slots
+        free_left = torch.empty(1, **new) if free_left is None else free_left
+        _check(load().sparse_paged_plan(
+            ctypes.byref(sh), _ptr(new_lens), _ptr(lens), _ptr(block_table), _ptr(free_pages), F,
+            _ptr(free_count), _ptr(kv_lens), _ptr(q_start), _ptr(positions), _ptr(slots),
+            _ptr(free_left), *scratch.args()), "paged_plan")
+        scratch.finish(check)
+    return {"kv_lens": kv_lens, "q_start": q_start, "positions": positions, "slots": slots,
+            "free_left": free_left}
+
+
+def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: bool = True):
+    """Write the new tokens' rows k_new, v_new [T,Hkv,d] (column ranges of
+    wider rows are fine) to their slots [T] int32 of the paged caches K, V
+    [num_pages,Hkv,page_size,d]; rows with slot -1 are skipped, and the other
+    slots are distinct."""
+    dev = _one_device(K, V, k_new, v_new, slots)
+    pages, Hkv, page, d = _cache_dims(K, V)
+    if not (k_new.dtype == v_new.dtype == K.dtype):
+        raise ValueError("K, V, k_new and v_new must share a dtype")
+    ks, vs = _rows(k_new, "k_new", Hkv, d), _rows(v_new, "v_new", Hkv, d)
+    T = k_new.shape[0]
+    if v_new.shape[0] != T:
+        raise ValueError("k_new and v_new must have the same rows")
+    _need_int32(slots, (T,), "slots")
+    sh = _shape(1, T, Hkv, Hkv, d, K.dtype, page, pages, 1)
+    if T == 0:
+        return
+    with torch.cuda.device(dev):
+        scratch = _Scratch(ws, dev, _HEADER, check)
+        _check(load().sparse_paged_append(ctypes.byref(sh), _ptr(K), _ptr(V), _ptr(k_new), ks,
+                                          _ptr(v_new), vs, _ptr(slots), *scratch.args()),
+               "paged_append")
+        scratch.finish(check)
+
+
+def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: int = 0,
+               max_new: int | None = None, ws: Workspace | None = None, check: bool = True,
+               return_lse: bool = True, out=None, lse=None):
+    """Attention of new tokens over their sequences' paged caches, themselves
+    included (sparse_paged_attn).
+
+    q [T,Hq,d]: the packed new tokens, sequence b's in rows q_start[b] to
+    q_start[b+1] - 1 (q_start [B+1], kv_lens [B] int32: what paged_plan
+    returned); row i stands at position p = kv_lens[b] - new tokens + i and
+    sees tokens j <= p, under ``window`` >= 1 only those with j > p - window
+    or j < ``sinks``.  max_new: the most new tokens one sequence has, if known
+    (1 for a decode step: the kernels for few rows need it).  Returns
+    (out [T,Hq,d], lse [T,Hq] or None); rows behind the last sequence are not
+    written."""
+    dev = _one_device(q, K, V, block_table, q_start, kv_lens, out, lse)
+    pages, Hkv, page, d = _cache_dims(K, V)
+    if q.dim() != 3 or q.dtype != K.dtype:
+        raise ValueError("q must be [T,Hq,d] of the cache's dtype")
+    T, Hq = q.shape[:2]
+    qs = _rows(q, "q", Hq, d)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B,max_blocks]")
+    B, blocks = block_table.shape
+    _need_int32(block_table, (B, blocks), "block_table")
+    _need_int32(q_start, (B + 1,), "q_start")
+    _need_int32(kv_lens, (B,), "kv_lens")
+    _need_result(out, (T, Hq, d), q.dtype, "out")
+    _need_result(lse, (T, Hq), torch.float32, "lse")
+    window, sinks = int(window), int(sinks)
+    if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+        raise ValueError("window and sinks must not be negative")
+    if max_new is not None and int(max_new) < 1:
+        raise ValueError("max_new must be at least 1")
+    sh = _shape(B, T, Hq, Hkv, d, q.dtype, page, pages, blocks, int(max_new or 0))
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+        if lse is None and return_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        n = ctypes.c_size_t(0)
+        _check(load().sparse_paged_workspace_size(ctypes.byref(sh), ctypes.byref(n)),
+               "paged_attn")
+        if T == 0:
+            return out, lse
+        scratch = _Scratch(ws, dev, int(n.value), check)
+        _check(load().sparse_paged_attn(
+            ctypes.byref(sh), _ptr(q), qs, _ptr(K), _ptr(V), _ptr(block_table), _ptr(q_start),
+            _ptr(kv_lens), window, sinks, _ptr(out), _ptr(lse), *scratch.args()), "paged_attn")
+        scratch.finish(check)
+    return out, lse
