@@ -48,6 +48,14 @@ struct PgArgs {
   int part_rows;
 };
 
+// 2^x by the hardware approximation (relative error about 2^-22; results
+// below 2^-126 flush to zero, which a softmax weight does not notice).
+__device__ __forceinline__ float pg_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The key tiles a block of tokens [t0, t1) of a sequence reads: tiles
 // [0, sink_tiles) and [lo, hi), KT keys each.
 struct PgTiles {

@@ -18,6 +18,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 constexpr size_t kPagedHeader = 4096;
 constexpr size_t kPagedScratch = kPagedHeader + (size_t)256 * kHistBins * sizeof(uint32_t);
 constexpr int kPartialSlots = 592;  // four pieces for each of 148 SMs
+static_assert(kPartialSlots >= 2 * kPagedMaxRuns, "two partials per decode run");
 
 sparse_status_t check_paged(const sparse_paged_shape_t *p, PagedShape *s) {
   if (!p) return SPARSE_ERR_INVALID_ARG;
@@ -47,7 +48,10 @@ PagedLayout layout(const PagedShape &s) {
   l.part_rows = (int)(rows < 256 ? rows : 256);
   l.head_off = kPagedScratch;
   l.seqs_off = l.head_off + up256(sizeof(PgHead));
-  l.arrive_off = l.seqs_off + up256((size_t)(s.B + 1) * sizeof(PgSeq));
+  // the schedule: one entry per sequence and one more, or one per decode run
+  const size_t entries = s.B + 1 > kPagedMaxRuns ? s.B + 1 : kPagedMaxRuns;
+  l.arrive_off = l.seqs_off + up256(entries * sizeof(PgSeq));
+  // counters and partials: slot_cap * Hkv >= kPartialSlots >= 2 * kPagedMaxRuns
   l.part_off = l.arrive_off + up256((size_t)l.slot_cap * s.Hkv * sizeof(uint32_t));
   l.total = l.part_off + up256((size_t)l.slot_cap * s.Hkv * l.part_rows * (s.d + 2) *
                                sizeof(float));
@@ -177,7 +181,10 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
   a.part = reinterpret_cast<float *>(w + l.part_off);
   a.slot_cap = l.slot_cap;
   a.part_rows = l.part_rows;
-  return sd::status_of(sd::launch_paged_attn_simt(s, a, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s.dtype == SPARSE_DTYPE_BF16 && s.max_new * s.G() <= 16)
+    return sd::status_of(sd::launch_paged_decode(s, a, st));
+  return sd::status_of(sd::launch_paged_attn_simt(s, a, st));
 }
 
 }  // extern "C"
