@@ -27,6 +27,8 @@ constexpr int kPagedMaxRuns = 256;
 
 // bf16, at most 16 query rows per (sequence, KV head) (paged_decode.cu).
 cudaError_t launch_paged_decode(const PagedShape &s, const PgArgs &a, cudaStream_t st);
+// bf16, any number of rows (paged_chunk.cu): tcgen05.
+cudaError_t launch_paged_chunk(const PagedShape &s, const PgArgs &a, cudaStream_t st);
 // fp32 inputs (paged_attn.cu): CUDA cores.
 cudaError_t launch_paged_attn_simt(const PagedShape &s, const PgArgs &a, cudaStream_t st);
 // The work items' schedule for row blocks of `tb` tokens, key tiles of `kt`

@@ -182,9 +182,9 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
   a.slot_cap = l.slot_cap;
   a.part_rows = l.part_rows;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (s.dtype == SPARSE_DTYPE_BF16 && s.max_new * s.G() <= 16)
-    return sd::status_of(sd::launch_paged_decode(s, a, st));
-  return sd::status_of(sd::launch_paged_attn_simt(s, a, st));
+  if (s.dtype == SPARSE_DTYPE_F32) return sd::status_of(sd::launch_paged_attn_simt(s, a, st));
+  return sd::status_of(s.max_new * s.G() <= 16 ? sd::launch_paged_decode(s, a, st)
+                                               : sd::launch_paged_chunk(s, a, st));
 }
 
 }  // extern "C"

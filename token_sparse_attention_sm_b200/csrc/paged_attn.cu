@@ -1,11 +1,11 @@
-// paged_attn.cu -- attention of new tokens over a paged cache on the CUDA
+// paged_attn.cu -- attention of new tokens over a paged fp32 cache on the CUDA
 // cores: o_i = sum_j softmax(z_i)_j v_j, z_ij = <q_i, k_j> / sqrt(d) over the
 // keys row i sees, one pass over the keys with a running maximum m and sum l
 // (when a tile raises m, o and l are scaled by exp2(m_old - m_new)).
 //
 // A worker (CTA) claims items of the schedule: a block of RB query rows of
 // one (sequence, KV head) and a piece of its key tiles.  Each tile of 64 keys
-// is copied into shared memory as fp32, K for S = Q K^T and V for O += P V
+// is copied into shared memory, K for S = Q K^T and V for O += P V
 // in turn, the next tile's K arriving while V is used and the other way round.
 // Thread (ty, tx) holds rows ty*4 .. +3 and keys tx + TX*j of S, then columns
 // of O; a row's TX threads are in one warp, so its maximum and sum are warp
@@ -42,11 +42,11 @@ __device__ __forceinline__ void cp16(void *dst, const void *src, bool pred) {
 // keys [key0, key0 + 64) of the sequence, those in [0, limit) that any row of
 // the block sees (j >= low or j < sinks), into dst as fp32 rows; zeros for
 // the others and for pages outside the pool.  kok (nullable): which were read.
-template <typename T, int D, int KS, int THREADS>
-__device__ __forceinline__ void load_tile(float *dst, unsigned char *kok, const T *cache,
+template <int D, int KS, int THREADS>
+__device__ __forceinline__ void load_tile(float *dst, unsigned char *kok, const float *cache,
                                           const PgArgs &a, const int *table, int h, int key0,
                                           int limit, int low) {
-  constexpr int PER = 16 / sizeof(T);  // elements of a 16-byte piece
+  constexpr int PER = 4;  // elements of a 16-byte piece
   constexpr int CPR = D / PER;
   for (int p = threadIdx.x; p < kKT * CPR; p += THREADS) {
     const int r = p / CPR, c = p % CPR;
@@ -60,21 +60,12 @@ __device__ __forceinline__ void load_tile(float *dst, unsigned char *kok, const 
       else if (c == 0) raise_flag(a.status, FLAG_INDEX);
     }
     if (kok && c == 0) kok[r] = ok;
-    if constexpr (sizeof(T) == 4) {
-      cp16(dst + r * KS + c * PER, cache + off, ok);
-    } else {
-      float f[PER];
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (ok) v = *reinterpret_cast<const uint4 *>(cache + off);
-      unpack16<T>(v, f);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) dst[r * KS + c * PER + i] = f[i];
-    }
+    cp16(dst + r * KS + c * PER, cache + off, ok);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-template <typename T, int D, int RB>
+template <int D, int RB>
 __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kernel(const PgArgs a) {
   using C = SimtCfg<D, RB>;
   constexpr int TX = C::TX, NK = C::NK, NC = C::NC, QS = C::QS, KS = C::KS, PS = C::PS;
@@ -85,9 +76,9 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
   unsigned char *kok = reinterpret_cast<unsigned char *>(box + 16);
   const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
   const int G = a.Hq / a.Hkv, TB = RB / G;
-  const T *q = static_cast<const T *>(a.q), *K = static_cast<const T *>(a.K),
-          *V = static_cast<const T *>(a.V);
-  T *out = static_cast<T *>(a.out);
+  const float *q = static_cast<const float *>(a.q), *K = static_cast<const float *>(a.K),
+              *V = static_cast<const float *>(a.V);
+  float *out = static_cast<float *>(a.out);
   grid_dep_wait();
   grid_dep_launch();
   const int per_head = a.seqs[a.B].base;
@@ -117,9 +108,8 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
       const int r = p / (D / 4), c = p % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
-        const T *src = q + (size_t)(row0 + t0 + r / G) * a.q_stride + (h * G + r % G) * D + c * 4;
-        v = make_float4(DT<T>::to_f(src[0]), DT<T>::to_f(src[1]), DT<T>::to_f(src[2]),
-                        DT<T>::to_f(src[3]));
+        const float *src = q + (size_t)(row0 + t0 + r / G) * a.q_stride + (h * G + r % G) * D + c * 4;
+        v = *reinterpret_cast<const float4 *>(src);
       }
       *reinterpret_cast<float4 *>(Qs + r * QS + c * 4) = v;
     }
@@ -139,10 +129,10 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
       lowr[i] = pg_window_low(pos[i], a.window);
     }
     if (u0 < u1)
-      load_tile<T, D, KS, THREADS>(Ks, kok, K, a, table, h, tiles.tile(u0) * kKT, limit, low);
+      load_tile<D, KS, THREADS>(Ks, kok, K, a, table, h, tiles.tile(u0) * kKT, limit, low);
     for (int u = u0; u < u1; ++u) {
       const int key0 = tiles.tile(u) * kKT;
-      load_tile<T, D, KS, THREADS>(Vs, nullptr, V, a, table, h, key0, limit, low);
+      load_tile<D, KS, THREADS>(Vs, nullptr, V, a, table, h, key0, limit, low);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
       float s[4][NK];
@@ -198,7 +188,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
       }
       __syncthreads();  // K is used up, P complete
       if (u + 1 < u1)
-        load_tile<T, D, KS, THREADS>(Ks, kok, K, a, table, h, tiles.tile(u + 1) * kKT, limit, low);
+        load_tile<D, KS, THREADS>(Ks, kok, K, a, table, h, tiles.tile(u + 1) * kKT, limit, low);
       else
         asm volatile("cp.async.commit_group;" ::: "memory");
       asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -245,7 +235,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const int col = (c / C::VEC) * (TX * C::VEC) + tx * C::VEC + c % C::VEC;
-          out[(tok * a.Hq + hq) * D + col] = DT<T>::from_f(o[i][c] * inv);
+          out[(tok * a.Hq + hq) * D + col] = o[i][c] * inv;
         }
         if (a.lse && tx == 0)
           a.lse[tok * a.Hq + hq] =
@@ -295,7 +285,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
           const size_t tok = (size_t)(row0 + t0 + r / G), hq = h * G + r % G;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
-            out[(tok * a.Hq + hq) * D + c * 32 + lane] = DT<T>::from_f(acc[c] * inv);
+            out[(tok * a.Hq + hq) * D + c * 32 + lane] = acc[c] * inv;
           if (a.lse && lane == 0)
             a.lse[tok * a.Hq + hq] =
                 ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
@@ -306,10 +296,10 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
   }
 }
 
-template <typename T, int D, int RB>
+template <int D, int RB>
 cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   using C = SimtCfg<D, RB>;
-  auto kern = paged_attn_simt_kernel<T, D, RB>;
+  auto kern = paged_attn_simt_kernel<D, RB>;
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
@@ -333,17 +323,16 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t pick(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   // up to 16 rows per (sequence, KV head): the cache is read once, memory bound
-  return s.max_new * s.G() <= 16 ? run<T, D, 16>(s, a, st) : run<T, D, 64>(s, a, st);
+  return s.max_new * s.G() <= 16 ? run<D, 16>(s, a, st) : run<D, 64>(s, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn_simt(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
-  if (s.dtype == 0) return s.d == 64 ? pick<float, 64>(s, a, st) : pick<float, 128>(s, a, st);
-  return s.d == 64 ? pick<__nv_bfloat16, 64>(s, a, st) : pick<__nv_bfloat16, 128>(s, a, st);
+  return s.d == 64 ? pick<64>(s, a, st) : pick<128>(s, a, st);
 }
 
 }  // namespace sd

@@ -1,0 +1,720 @@
+// paged_chunk.cu -- paged attention in bf16 for blocks of many query rows (a
+// prompt's chunk; any batch whose sequences may have more than 16 rows per KV
+// head): S = Q K^T and O += P V on the 5th-generation tensor cores.
+//
+// One persistent CTA per SM claims items of the schedule: a block of up to
+// 256 query rows of one (sequence, KV head) -- two tiles of 128, row r of a
+// tile being token r / G, head r % G -- and a piece of its 128-key tiles.
+// Both row tiles use every K and V tile, which halves what one reads from L2
+// (at 128 rows the tile loads alone would ask for more than L2 gives).
+//
+// Roles (384 threads, two warps idle):
+//  * a TMA warp claims items and streams Q, then K and V tiles through a ring
+//    (one copy per page fragment and 64 columns, 128-byte swizzle);
+//  * one thread issues the MMAs: S_t = Q_t K^T (M = N = 128) and O_t += P_t V,
+//    P_t read from tensor memory;
+//  * four softmax warps per row tile, one row per thread: S from tensor
+//    memory, the row's maximum, P = exp2(S scale - m) rounded to bf16 over the
+//    dead S, and O scaled when the maximum moves.
+// The two row tiles alternate: while one's softmax runs, the other's products
+// do.  Tensor memory: S_0, S_1, O_0, O_1 (512 columns at d = 128).
+//
+// The reference m of a row is only raised when the running maximum has left it
+// by more than 2^8: weights then reach 256 instead of 1, the sums stay fp32,
+// the division at the end cancels m, and O is almost never rescaled.
+// P is rounded to bf16 (2^-9 of each weight on average, independent errors
+// that the sum over keys averages; the result is rounded to bf16 anyway); its
+// sum is taken before the rounding.
+//
+// Every wait is bounded; when one runs out the kernel raises TIMEOUT, all
+// roles leave their loops, the tensor memory is freed and the kernel returns.
+#include "paged.h"
+#include "paged.cuh"
+#include "paged_tma.h"
+
+namespace sd {
+namespace {
+
+constexpr int kChKeys = 128;
+constexpr int kChSoftWarps = 8;
+constexpr int kChThreads = 384;  // three warpgroups: two of softmax warps, TMA + MMA (+ two idle)
+// registers a thread: 168 at launch, moved from the third warpgroup to the
+// softmax ones (2 * 128 * 200 + 128 * 104 = 384 * 168)
+constexpr int kChSoftRegs = 200, kChOtherRegs = 104;
+constexpr int kChMmaWarp = kChSoftWarps, kChTmaWarp = kChSoftWarps + 1;
+constexpr float kChLag = 8.f;  // log2 units the maximum may run ahead of its reference
+
+template <int D>
+struct ChCfg {
+  static constexpr int CB = D / 64;
+  static constexpr int kQTile = 128 * D * 2;
+  static constexpr int kTile = kChKeys * D * 2;  // K or V of a tile: one ring slot
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kQOff = 0, kRingOff = 2 * kQTile;
+  static constexpr int kSmallOff = kRingOff + kSlots * kTile;
+  static constexpr int kSmem = kSmallOff + 1024 + 1024;  // small area, alignment slack
+};
+
+// One work item, as the TMA warp found it.
+struct ChItem {
+  int b, h, row0, t0, rows;            // rows: query rows of the block
+  int p_first, p_last, low;            // positions of its first and last token; lowest key of a window
+  int u0, u1;                          // the piece's tiles
+  int sink_tiles, lo;
+  int np, piece, first;                // partial slots: (first + piece) * Hkv + h
+  int valid;                           // 0: no more items
+};
+
+struct ChSmall {
+  uint64_t full[8], empty[8];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_ready[2], pv_done[2], o_empty[2], wg[2];
+  uint64_t item_full[2], item_empty[2];
+  ChItem item[2];
+  uint32_t ok[8];
+  uint32_t tmem, abort, last[2];
+};
+static_assert(sizeof(ChSmall) <= 1024, "small area");
+
+// ---- tcgen05 ------------------------------------------------------------------
+__device__ __forceinline__ void ch_ld32(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void ch_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void ch_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void ch_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void ch_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void ch_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// shared-memory matrix descriptor, 128-byte swizzle (sm_100 version)
+__device__ __forceinline__ uint64_t ch_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16, bf16 operands, fp32 accumulator, M = 128
+__host__ __device__ constexpr uint32_t ch_idesc(int N, bool b_mn_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void ch_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A in tensor memory: lane = row, two bf16 per column
+__device__ __forceinline__ void ch_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void ch_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void ch_tma(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                       uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ uint32_t ch_pack(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// bits 0 .. n-1 of a word
+__device__ __forceinline__ uint32_t ch_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Wait for a phase; false once any wait of the CTA has run out.
+__device__ __forceinline__ bool ch_wait(uint64_t *bar, uint32_t parity, ChSmall *sm,
+                                        uint32_t *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  volatile uint32_t *abort = &sm->abort;
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      raise_flag(status, FLAG_TIMEOUT);
+      *abort = 1u;
+      return false;
+    }
+  }
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChThreads, 1)
+    paged_chunk_kernel(const PgArgs a, const __grid_constant__ CUtensorMap mapQ,
+                       const __grid_constant__ CUtensorMap mapK,
+                       const __grid_constant__ CUtensorMap mapV, int frag_rows) {
+  using C = ChCfg<D>;
+  extern __shared__ unsigned char raw[];
+  const uint32_t raw_s = smem_u32(raw);
+  const uint32_t base = (raw_s + 1023u) & ~1023u;
+  ChSmall *sm = reinterpret_cast<ChSmall *>(raw + (base - raw_s) + C::kSmallOff);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.Hq / a.Hkv, TPT = 128 / G, TB = 2 * TPT;  // tokens per row tile, per block
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sm->tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    sm->abort = 0;
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&sm->full[i], 1);
+      mbar_init(&sm->empty[i], 1);
+    }
+    mbar_init(&sm->q_full, 1);
+    mbar_init(&sm->q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm->s_full[t], 1);
+      mbar_init(&sm->p_ready[t], 4);
+      mbar_init(&sm->pv_done[t], 1);
+      mbar_init(&sm->o_empty[t], 4);
+      mbar_init(&sm->wg[t], 4);
+      mbar_init(&sm->item_full[t], 1);
+      mbar_init(&sm->item_empty[t], kChSoftWarps + 1);
+    }
+    fence_mbar_init();
+  }
+  ch_fence_before();
+  __syncthreads();
+  ch_fence_after();
+  grid_dep_wait();
+  grid_dep_launch();
+  const uint32_t tmem = sm->tmem;
+
+  if (warp >= kChSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChOtherRegs));
+    if (warp == kChTmaWarp) {
+      // ---- TMA warp: items, Q, K and V ----------------------------------------------
+      const int per_head = a.seqs[a.B].base;
+      const long long total = (long long)per_head * a.Hkv;
+      const int nfrag = kChKeys / frag_rows, per = 32 / nfrag;
+      int slot = 0, unit = 0, q_count = 0;
+      uint32_t phase = 0;
+      bool alive = true;
+      for (int it = 0; alive; ++it) {
+        uint32_t x = 0;
+        if (lane == 0) x = atomicAdd(&a.head->next, 1u);
+        x = __shfl_sync(0xffffffffu, x, 0);
+        ChItem &I = sm->item[it & 1];
+        if (!__all_sync(0xffffffffu,
+                        ch_wait(&sm->item_empty[it & 1], ((it >> 1) & 1) ^ 1, sm, a.status)))
+          break;
+        const bool valid = x < total;
+        if (valid) {
+          const int y = (int)(x % (uint32_t)per_head);
+          PgSeq sq;
+          const int b = pg_find(a.seqs, a.B, y, &sq);
+          if (lane == 0) {
+            int row0, n, kv;
+            pg_lengths(a, b, &row0, &n, &kv);
+            const int nrb = (n + TB - 1) / TB;
+            // piece-major, the blocks with the longest ranges first
+            const int piece = (y - sq.base) / nrb, rb = nrb - 1 - (y - sq.base) % nrb;
+            const int t0 = rb * TB, t1 = min(n, t0 + TB);
+            const int p_first = kv - n + t0, p_last = kv - n + t1 - 1;
+            const PgTiles t = pg_tiles(p_first, p_last, a.window, a.sinks, kChKeys);
+            I.b = b;
+            I.h = (int)(x / (uint32_t)per_head);
+            I.row0 = row0;
+            I.t0 = t0;
+            I.rows = (t1 - t0) * G;
+            I.p_first = p_first;
+            I.p_last = p_last;
+            I.low = pg_window_low(p_first, a.window);
+            I.sink_tiles = t.sink_tiles;
+            I.lo = t.lo;
+            I.u0 = min(piece * sq.len, t.units());
+            I.u1 = min(t.units(), I.u0 + sq.len);
+            I.np = sq.np;
+            I.piece = piece;
+            I.first = sq.slot + rb * sq.np;
+          }
+        }
+        if (lane == 0) {
+          I.valid = valid;
+          mbar_arrive(&sm->item_full[it & 1]);
+        }
+        __syncwarp();
+        if (!valid) break;
+        const int u0 = I.u0, u1 = I.u1, h = I.h, low = I.low, limit = I.p_last + 1;
+        const int sink_tiles = I.sink_tiles, lo = I.lo;
+        if (u0 >= u1) continue;
+        // Q: the block's one or two row tiles
+        if (!__all_sync(0xffffffffu, ch_wait(&sm->q_empty, (q_count & 1) ^ 1, sm, a.status))) break;
+        ++q_count;
+        if (lane == 0) {
+          const int tiles = I.rows > TPT * G ? 2 : 1;
+          mbar_arrive_expect_tx(&sm->q_full, tiles * C::CB * TPT * G * 128);
+          for (int t = 0; t < tiles; ++t)
+            for (int c = 0; c < C::CB; ++c)
+              ch_tma(base + C::kQOff + t * C::kQTile + c * (128 * 128), &mapQ, c * 64, h * G,
+                     I.row0 + I.t0 + t * TPT, &sm->q_full);
+        }
+        __syncwarp();
+        const int *table = a.table + (size_t)I.b * a.blocks;
+        auto key_of = [&](int u) {
+          return (u < sink_tiles ? u : u - sink_tiles + lo) * kChKeys;
+        };
+        // lane i: table entry of fragment i % nfrag of tile ub + i / nfrag; -1: not read
+        auto fetch = [&](int ub) {
+          const int u = ub + lane / nfrag;
+          int e = -1;
+          if (lane < per * nfrag && u < u1) {
+            const int j0 = key_of(u) + (lane % nfrag) * frag_rows;
+            if (j0 < limit && (j0 + frag_rows > low || j0 < a.sinks)) {
+              e = table[j0 / a.page];
+              if (e < 0 || e >= a.pages) {
+                raise_flag(a.status, FLAG_INDEX);
+                e = -2;
+              }
+            }
+          }
+          return e;
+        };
+        int next = fetch(u0);
+        for (int ub = u0; ub < u1 && alive; ub += per) {
+          const int cur = next;
+          next = fetch(ub + per);
+          for (int u = ub; u < min(u1, ub + per) && alive; ++u) {
+            const int e = __shfl_sync(0xffffffffu, cur, (u - ub) * nfrag + lane % nfrag);
+            const uint32_t bad = __ballot_sync(0xffffffffu, lane < nfrag && e == -2);
+            const int j0 = key_of(u) + (lane % nfrag) * frag_rows;
+            const int y = e >= 0 ? j0 % a.page : 0;
+            const int z = e >= 0 ? e * a.Hkv + h : a.pages * a.Hkv;  // past the pool: zeros
+            for (int kv = 0; kv < 2; ++kv) {
+              if (!__all_sync(0xffffffffu, ch_wait(&sm->empty[slot], phase ^ 1u, sm, a.status))) {
+                alive = false;
+                break;
+              }
+              if (lane == 0) {
+                if (kv == 0) {  // one bit per 16 keys
+                  uint32_t ok16 = 0;
+                  for (int i = 0; i < kChKeys / 16; ++i)
+                    ok16 |= (~(bad >> (i * 16 / frag_rows)) & 1u) << i;
+                  sm->ok[unit & 7] = ok16;
+                }
+                mbar_arrive_expect_tx(&sm->full[slot], C::kTile);
+              }
+              __syncwarp();
+              if (lane < nfrag) {
+                const uint32_t dst = base + C::kRingOff + slot * C::kTile + lane * frag_rows * 128;
+  #pragma unroll
+                for (int c = 0; c < C::CB; ++c)
+                  ch_tma(dst + c * (kChKeys * 128), kv ? &mapV : &mapK, c * 64, y, z,
+                         &sm->full[slot]);
+              }
+              __syncwarp();
+              if (++slot == C::kSlots) slot = 0, phase ^= 1u;
+            }
+            ++unit;
+          }
+        }
+      }
+    } else if (warp == kChMmaWarp) {
+      // ---- MMA thread ------------------------------------------------------------------
+      if (lane == 0) {
+        constexpr uint32_t idS = ch_idesc(kChKeys, false), idPV = ch_idesc(D, true);
+        int slot = 0;                 // ring position of the next K tile
+        uint32_t phase = 0;
+        int q_count = 0;              // items with tiles so far
+        uint32_t p_cnt[2] = {0, 0}, pv_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};
+        bool ok = true;
+        auto step = [&]() {
+          if (++slot == C::kSlots) slot = 0, phase ^= 1u;
+        };
+        auto issue_s = [&](int t, int kslot) {
+          const uint64_t q = ch_desc(base + C::kQOff + t * C::kQTile, 16, 1024);
+          const uint64_t k = ch_desc(base + C::kRingOff + kslot * C::kTile, 16, 1024);
+  #pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            // the address field of a descriptor counts 16-byte units
+            const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) / 16;
+            ch_mma_ss(tmem + t * 128, q + off, k + off, idS, s > 0);
+          }
+          ch_commit(&sm->s_full[t]);
+        };
+        for (int it = 0;; ++it) {
+          if (!ch_wait(&sm->item_full[it & 1], (it >> 1) & 1, sm, a.status)) break;
+          const ChItem &I = sm->item[it & 1];
+          const int valid = I.valid, n = I.u1 - I.u0, tiles = I.rows > TPT * G ? 2 : 1;
+          mbar_arrive(&sm->item_empty[it & 1]);
+          if (!valid) break;
+          if (n <= 0) continue;
+          if (!(ok = ch_wait(&sm->q_full, q_count & 1, sm, a.status))) break;
+          ++q_count;
+          // S of the first key tile
+          if (!(ok = ch_wait(&sm->full[slot], phase, sm, a.status))) break;
+          for (int t = 0; t < tiles && ok; ++t) {
+            // the last P of the item before is used up
+            if (pv_cnt[t] > 0) ok = ch_wait(&sm->pv_done[t], (pv_cnt[t] - 1) & 1, sm, a.status);
+            if (!ok) break;
+            ch_fence_after();
+            issue_s(t, slot);
+          }
+          if (!ok) break;
+          ch_commit(&sm->empty[slot]);
+          if (n == 1) ch_commit(&sm->q_empty);
+          step();
+          for (int j = 0; j < n && ok; ++j) {
+            const int vslot = slot;
+            const uint32_t vphase = phase;
+            step();  // slot: the next K
+            for (int t = 0; t < tiles && ok; ++t) {
+              ok = ch_wait(&sm->p_ready[t], p_cnt[t] & 1, sm, a.status);
+              ++p_cnt[t];
+              if (ok && t == 0) ok = ch_wait(&sm->full[vslot], vphase, sm, a.status);
+              // O of the item before has been read
+              if (ok && j == 0 && o_cnt[t] > 0)
+                ok = ch_wait(&sm->o_empty[t], (o_cnt[t] - 1) & 1, sm, a.status);
+              if (j == 0) ++o_cnt[t];
+              if (!ok) break;
+              ch_fence_after();
+              const uint64_t v =
+                  ch_desc(base + C::kRingOff + vslot * C::kTile, kChKeys * 128, 1024);
+  #pragma unroll
+              for (int kk = 0; kk < kChKeys / 16; ++kk)
+                ch_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
+                          v + kk * (2048 / 16), idPV, j > 0 || kk > 0);
+              ch_commit(&sm->pv_done[t]);
+              ++pv_cnt[t];
+              if (t == tiles - 1) ch_commit(&sm->empty[vslot]);
+              if (j + 1 < n) {
+                if (t == 0) ok = ch_wait(&sm->full[slot], phase, sm, a.status);
+                // S_t overwrites the P_t that the product just issued reads
+                if (ok) ok = ch_wait(&sm->pv_done[t], (pv_cnt[t] - 1) & 1, sm, a.status);
+                if (!ok) break;
+                ch_fence_after();
+                issue_s(t, slot);
+                if (t == tiles - 1) {
+                  ch_commit(&sm->empty[slot]);
+                  if (j + 2 == n) ch_commit(&sm->q_empty);
+                }
+              }
+            }
+            if (j + 1 < n) step();
+          }
+          if (!ok) break;
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChSoftRegs));
+    // ---- softmax warps: tile t, one row per thread -----------------------------------
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + 256 + t * 128;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
+    int ring = 0;  // ring position of the next K tile, and the phase of its round
+    uint32_t phase = 0, s_cnt = 0, wg_cnt = 0;
+    int unit = 0;
+    bool ok = true;
+    constexpr uint32_t all_ok = (1u << (kChKeys / 16)) - 1u;
+    auto step = [&]() {
+      if (++ring == C::kSlots) ring = 0, phase ^= 1u;
+    };
+    // the four warps of the tile meet (bounded)
+    auto wg_sync = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->wg[t]);
+      const bool w = ch_wait(&sm->wg[t], wg_cnt & 1, sm, a.status);
+      ++wg_cnt;
+      return w;
+    };
+    for (int it = 0;; ++it) {
+      if (!ch_wait(&sm->item_full[it & 1], (it >> 1) & 1, sm, a.status)) break;
+      const ChItem &I = sm->item[it & 1];  // until this warp's arrival below
+      auto done = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->item_empty[it & 1]);
+      };
+      if (!I.valid) break;
+      const int n = max(0, I.u1 - I.u0), tile_rows = TPT * G;
+      if (t == 1 && I.rows <= tile_rows) {  // no second row tile: keep count of the ring
+        for (int j = 0; j < n; ++j) step(), step();
+        unit += n;
+        done();
+        continue;
+      }
+      const int br = t * tile_rows + r;  // row of the block
+      const bool live = r < tile_rows && br < I.rows;
+      const int pos = live ? I.p_first + br / G : -1;
+      const int low = pg_window_low(pos, a.window);
+      const int pf = I.p_first + t * TPT, pl = min(I.p_last, pf + TPT - 1);  // the tile's tokens
+      const int low_last = pg_window_low(pl, a.window);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        const int u = I.u0 + j;
+        const int key0 = (u < I.sink_tiles ? u : u - I.sink_tiles + I.lo) * kChKeys;
+        step();
+        const int vslot = ring;
+        const uint32_t vphase = phase;
+        step();
+        ok = ch_wait(&sm->s_full[t], s_cnt & 1, sm, a.status);
+        ++s_cnt;
+        // also orders this after the TMA warp's note on the tile's pages
+        if (ok) ok = ch_wait(&sm->full[vslot], vphase, sm, a.status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ch_fence_after();
+        const uint32_t good = sm->ok[unit & 7];
+        ++unit;
+        if (t == 0 && (key0 + kChKeys > I.p_last + 1 || (key0 < I.low && key0 + kChKeys > a.sinks))) {
+          // V rows that no row of the block sees may hold anything: clear them
+          const int key = key0 + r;
+          if (key > I.p_last || (key < I.low && key >= a.sinks)) {
+            const uint32_t v = base + C::kRingOff + vslot * C::kTile + r * 128;
+#pragma unroll
+            for (int c = 0; c < C::CB; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                 v + c * (kChKeys * 128) + i * 16),
+                             "r"(0u)
+                             : "memory");
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ch_ld32(tS + c * 32, s + c * 32);
+        ch_wait_ld();
+        if (key0 + kChKeys - 1 > pf || (key0 < low_last && key0 + kChKeys > a.sinks) ||
+            good != all_ok) {
+          // the row's keys of the tile, a bit each
+          const int hi = pos - key0, lo = low - key0, sk = a.sinks - key0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t pages = ((good >> (2 * w)) & 1u ? 0xffffu : 0u) |
+                                   ((good >> (2 * w)) & 2u ? 0xffff0000u : 0u);
+            const uint32_t see = ch_below(hi + 1 - 32 * w) &
+                                 (~ch_below(lo - 32 * w) | ch_below(sk - 32 * w)) & pages;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((see >> i) & 1u)) s[w * 32 + i] = 0xff800000u;
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
+        mx *= a.scale_log2;
+        const bool raise = mx > m + kChLag || (m == -INFINITY && mx > m);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float mn = raise ? mx : m;
+          const float corr = raise ? exp2f(m - mn) : 1.f;  // 0 for the first tile
+          m = mn;
+          l *= corr;
+          if (j > 0) {
+            // the product before has finished: S of this tile came after it
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              ch_ld32(tO + c * 32, o);
+              ch_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+              ch_st32(tO + c * 32, o);
+            }
+          }
+        }
+        const float use = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int k = c * 64 + i * 2;
+            const float p0 = pg_exp2(fmaf(__uint_as_float(s[k]), a.scale_log2, -use));
+            const float p1 = pg_exp2(fmaf(__uint_as_float(s[k + 1]), a.scale_log2, -use));
+            sum[i & 3] += p0 + p1;
+            p[i] = ch_pack(p0, p1);
+          }
+          ch_st32(tS + c * 32, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        ch_wait_st();
+        ch_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->p_ready[t]);
+      }
+      if (!ok) break;
+      // ---- the piece's result ----------------------------------------------------------
+      if (n > 0) {
+        // every product of the item is done when its last one is
+        ok = ch_wait(&sm->pv_done[t], (s_cnt - 1) & 1, sm, a.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        ch_fence_after();
+      }
+      const size_t at = (size_t)(I.row0 + I.t0 + br / G) * a.Hq + I.h * G + br % G;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const size_t per = (size_t)a.part_rows * D;
+      const size_t first = (size_t)I.first * a.Hkv + I.h;
+      const size_t mine = first + (size_t)I.piece * a.Hkv;
+      float2 *ml = reinterpret_cast<float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          ch_ld32(tO + c * 32, o);
+          ch_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (live) {
+          if (I.np == 1) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 pk;
+              uint32_t *w = &pk.x;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = ch_pack(__uint_as_float(o[i + 2 * e]) * inv,
+                               __uint_as_float(o[i + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4 *>(out + at * D + c * 32 + i) = pk;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4 *>(a.part + mine * per + (size_t)br * D + c * 32 + i) =
+                  make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+      }
+      ch_fence_before();
+      __syncwarp();
+      if (lane == 0 && n > 0) mbar_arrive(&sm->o_empty[t]);
+      if (I.np == 1) {
+        if (live && a.lse)
+          a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        done();
+        continue;
+      }
+      if (live) ml[mine * a.part_rows + br] = make_float2(m, l);
+      __threadfence();
+      if (!(ok = wg_sync())) break;
+      if (tid % 128 == 0)
+        sm->last[t] = atomicAdd(&a.arrive[first + (size_t)t * a.Hkv], 1u) == (uint32_t)(I.np - 1);
+      if (!(ok = wg_sync())) break;
+      if (sm->last[t]) {
+        // the block's last piece to arrive merges them all, in order; a warp per row
+        __threadfence();
+        const int rows_here = min(I.rows - t * tile_rows, tile_rows);
+        for (int rr = warp & 3; rr < rows_here; rr += 4) {
+          const int row = t * tile_rows + rr;
+          float mm = -INFINITY;
+          for (int p = 0; p < I.np; ++p)
+            mm = fmaxf(mm, __ldcg(&ml[(first + (size_t)p * a.Hkv) * a.part_rows + row].x));
+          const float us = mm == -INFINITY ? 0.f : mm;
+          float acc[D / 32] = {}, ll = 0.f;
+          for (int p = 0; p < I.np; ++p) {
+            const size_t sl = first + (size_t)p * a.Hkv;
+            const float2 e = __ldcg(&ml[sl * a.part_rows + row]);
+            const float f = exp2f(e.x - us);
+            ll += e.y * f;
+            if (f > 0.f) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c)
+                acc[c] += __ldcg(&a.part[sl * per + (size_t)row * D + c * 32 + lane]) * f;
+            }
+          }
+          const float iv = ll > 0.f ? 1.f / ll : 0.f;
+          const size_t o = (size_t)(I.row0 + I.t0 + row / G) * a.Hq + I.h * G + row % G;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+            out[o * D + c * 32 + lane] = __float2bfloat16_rn(acc[c] * iv);
+          if (a.lse && lane == 0)
+            a.lse[o] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+      if (!(ok = wg_sync())) break;  // sm->last is read before the next item's
+      done();
+    }
+  }
+  ch_fence_before();
+  __syncthreads();
+  ch_fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+}
+
+template <int D>
+cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
+  using C = ChCfg<D>;
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  auto kern = paged_chunk_kernel<D>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int frag = pg_part_rows(s.page, s.blocks, kChKeys);
+  const int TPT = 128 / s.G();
+  CUtensorMap mq, mk, mv;
+  e = pg_query_map(&mq, a.q, D, s.Hq, s.T, a.q_stride, s.G(), TPT);
+  if (e == cudaSuccess) e = pg_cache_map(&mk, a.K, D, s.page, (long long)s.pages * s.Hkv, frag);
+  if (e == cudaSuccess) e = pg_cache_map(&mv, a.V, D, s.page, (long long)s.pages * s.Hkv, frag);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_paged_schedule(s, a, 2 * TPT, kChKeys, di.sm_count, st)) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attrs[1];
+  cfg.stream = st;
+  cfg.attrs = attrs;
+  cfg.gridDim = dim3((unsigned)di.sm_count, 1, 1);
+  cfg.blockDim = dim3(kChThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.numAttrs = 0;
+  add_pdl_attr(cfg, attrs);
+  e = cudaLaunchKernelEx(&cfg, kern, a, mq, mk, mv, frag);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
+  return s.d == 64 ? run<64>(s, a, st) : run<128>(s, a, st);
+}
+
+}  // namespace sd
