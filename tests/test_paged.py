@@ -263,6 +263,17 @@ def test_attn_many_splits_and_steps(lib, dtype, max_new):
 
 @gpu
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("new", [1, 40])
+def test_attn_long_runs(lib, dtype, d, page, new):
+    """Runs of many tiles: every stage of a ring is reused several times."""
+    x = _batch([new, 1], [30000, 17], 8, 8, d, page, dtype, seed=d + new)
+    _assert_attn(x, sd.paged_attn(*x["args"], max_new=new))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_attn_rows_that_see_nothing(lib, dtype):
     # more new tokens than cached ones: the first rows stand before the cache
     x = _batch([5, 3, 200, 1], [2, 0, 150, 0], 8, 2, 64, 16, dtype)

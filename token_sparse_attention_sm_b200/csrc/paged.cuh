@@ -42,6 +42,10 @@ struct PgArgs {
   // schedule and partials (workspace)
   PgHead *head;
   PgSeq *seqs;
+  // decode: arrivals, zero between calls
+  uint32_t *runs;    // [kPagedMaxRuns] of a pair's runs, or its first group's, at its first run
+  uint32_t *groups;  // [kPagedMaxRuns] of another group's runs, at the group's first run
+  uint32_t *tops;    // [kPagedTops] of a pair's groups
   uint32_t *arrive;  // [slot_cap * Hkv], zeroed by the schedule kernel
   float *part;       // [slot_cap * Hkv][part_rows][d] then [..][part_rows] (max, sum)
   int slot_cap;      // partial slots per KV head
@@ -63,6 +67,11 @@ struct PgTiles {
   __device__ int units() const { return sink_tiles + hi - lo; }
   __device__ int tile(int u) const { return u < sink_tiles ? u : u - sink_tiles + lo; }
 };
+
+// bits 0 .. n-1 of a word
+__device__ __forceinline__ uint32_t pg_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
 
 // The first key that the window leaves a row at position p (0: no window).
 __device__ __forceinline__ int pg_window_low(int p, int window) {

@@ -23,7 +23,8 @@ struct PagedLayout {
 };
 
 // Runs that the decode kernel may cut its work into (two partials each).
-constexpr int kPagedMaxRuns = 256;
+constexpr int kPagedMaxRuns = 192;
+constexpr int kPagedTops = 12;
 
 // bf16, at most 16 query rows per (sequence, KV head) (paged_decode.cu).
 cudaError_t launch_paged_decode(const PagedShape &s, const PgArgs &a, cudaStream_t st);

@@ -2,10 +2,11 @@
 // checks on the host (an error returns before anything is enqueued), then the
 // kernels on the caller's stream.
 //
-// Workspace: the 4 KB header with the device status word first, the area that
-// the routing calls keep zero between calls (skipped, so that a workspace may
-// serve both), then the schedule and the partial results, which every call
-// writes before reading.
+// Workspace: the 4 KB header with the device status word first and the decode
+// runs' arrival counters (zero between calls) from bytes 128 and 3072, the area that the
+// routing calls keep zero between calls (skipped, so that a workspace may serve
+// both), then the schedule and the partial results, which every call writes
+// before reading.
 #include "paged.h"
 #include "paged.cuh"
 
@@ -15,7 +16,11 @@ namespace {
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-constexpr size_t kPagedHeader = 4096;
+constexpr size_t kPagedHeader = 4096, kRunsOff = 3072, kTopsOff = 128, kGroupsOff = 192;
+static_assert(kTopsOff + kPagedTops * sizeof(uint32_t) <= kGroupsOff &&
+                  kGroupsOff + kPagedMaxRuns * sizeof(uint32_t) <= 1024 &&
+                  kRunsOff + kPagedMaxRuns * sizeof(uint32_t) <= kPagedHeader,
+              "the counters fit around the routing scan's");
 constexpr size_t kPagedScratch = kPagedHeader + (size_t)256 * kHistBins * sizeof(uint32_t);
 constexpr int kPartialSlots = 592;  // four pieces for each of 148 SMs
 static_assert(kPartialSlots >= 2 * kPagedMaxRuns, "two partials per decode run");
@@ -48,10 +53,8 @@ PagedLayout layout(const PagedShape &s) {
   l.part_rows = (int)(rows < 256 ? rows : 256);
   l.head_off = kPagedScratch;
   l.seqs_off = l.head_off + up256(sizeof(PgHead));
-  // the schedule: one entry per sequence and one more, or one per decode run
-  const size_t entries = s.B + 1 > kPagedMaxRuns ? s.B + 1 : kPagedMaxRuns;
-  l.arrive_off = l.seqs_off + up256(entries * sizeof(PgSeq));
-  // counters and partials: slot_cap * Hkv >= kPartialSlots >= 2 * kPagedMaxRuns
+  l.arrive_off = l.seqs_off + up256((size_t)(s.B + 1) * sizeof(PgSeq));
+  // partials: slot_cap * Hkv >= kPartialSlots >= 2 * kPagedMaxRuns
   l.part_off = l.arrive_off + up256((size_t)l.slot_cap * s.Hkv * sizeof(uint32_t));
   l.total = l.part_off + up256((size_t)l.slot_cap * s.Hkv * l.part_rows * (s.d + 2) *
                                sizeof(float));
@@ -177,6 +180,9 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
   a.status = reinterpret_cast<uint32_t *>(w);
   a.head = reinterpret_cast<sd::PgHead *>(w + l.head_off);
   a.seqs = reinterpret_cast<sd::PgSeq *>(w + l.seqs_off);
+  a.runs = reinterpret_cast<uint32_t *>(w + sd::kRunsOff);
+  a.groups = reinterpret_cast<uint32_t *>(w + sd::kGroupsOff);
+  a.tops = reinterpret_cast<uint32_t *>(w + sd::kTopsOff);
   a.arrive = reinterpret_cast<uint32_t *>(w + l.arrive_off);
   a.part = reinterpret_cast<float *>(w + l.part_off);
   a.slot_cap = l.slot_cap;

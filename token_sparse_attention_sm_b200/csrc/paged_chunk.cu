@@ -8,9 +8,9 @@
 // Both row tiles use every K and V tile, which halves what one reads from L2
 // (at 128 rows the tile loads alone would ask for more than L2 gives).
 //
-// Roles (384 threads, two warps idle):
-//  * a TMA warp claims items and streams Q, then K and V tiles through a ring
-//    (one copy per page fragment and 64 columns, 128-byte swizzle);
+// Roles (384 threads, one warp idle):
+//  * two TMA warps, one of which claims the items and copies Q, stream K and V
+//    tiles through one ring (one copy per page and tile, 128-byte swizzle);
 //  * one thread issues the MMAs: S_t = Q_t K^T (M = N = 128) and O_t += P_t V,
 //    P_t read from tensor memory;
 //  * four softmax warps per row tile, one row per thread: S from tensor
@@ -37,11 +37,11 @@ namespace {
 
 constexpr int kChKeys = 128;
 constexpr int kChSoftWarps = 8;
-constexpr int kChThreads = 384;  // three warpgroups: two of softmax warps, TMA + MMA (+ two idle)
+constexpr int kChThreads = 384;  // three warpgroups: two of softmax warps; MMA, K and V copies, one idle
 // registers a thread: 168 at launch, moved from the third warpgroup to the
 // softmax ones (2 * 128 * 200 + 128 * 104 = 384 * 168)
 constexpr int kChSoftRegs = 200, kChOtherRegs = 104;
-constexpr int kChMmaWarp = kChSoftWarps, kChTmaWarp = kChSoftWarps + 1;
+constexpr int kChMmaWarp = kChSoftWarps, kChTmaWarp = kChSoftWarps + 1;  // K's, then V's
 constexpr float kChLag = 8.f;  // log2 units the maximum may run ahead of its reference
 
 template <int D>
@@ -151,11 +151,6 @@ __device__ __forceinline__ uint32_t ch_pack(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
-// bits 0 .. n-1 of a word
-__device__ __forceinline__ uint32_t ch_below(int n) {
-  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
 // Wait for a phase; false once any wait of the CTA has run out.
 __device__ __forceinline__ bool ch_wait(uint64_t *bar, uint32_t parity, ChSmall *sm,
                                         uint32_t *status) {
@@ -177,7 +172,7 @@ template <int D>
 __global__ void __launch_bounds__(kChThreads, 1)
     paged_chunk_kernel(const PgArgs a, const __grid_constant__ CUtensorMap mapQ,
                        const __grid_constant__ CUtensorMap mapK,
-                       const __grid_constant__ CUtensorMap mapV, int frag_rows) {
+                       const __grid_constant__ CUtensorMap mapV, const PgTile tl) {
   using C = ChCfg<D>;
   extern __shared__ unsigned char raw[];
   const uint32_t raw_s = smem_u32(raw);
@@ -208,9 +203,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
       mbar_init(&sm->o_empty[t], 4);
       mbar_init(&sm->wg[t], 4);
       mbar_init(&sm->item_full[t], 1);
-      mbar_init(&sm->item_empty[t], kChSoftWarps + 1);
+      mbar_init(&sm->item_empty[t], kChSoftWarps + 2);
     }
     fence_mbar_init();
+    pg_prefetch_map(&mapQ);
+    pg_prefetch_map(&mapK);
+    pg_prefetch_map(&mapV);
   }
   ch_fence_before();
   __syncthreads();
@@ -221,133 +219,152 @@ __global__ void __launch_bounds__(kChThreads, 1)
 
   if (warp >= kChSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChOtherRegs));
-    if (warp == kChTmaWarp) {
-      // ---- TMA warp: items, Q, K and V ----------------------------------------------
+    if (warp == kChTmaWarp || warp == kChTmaWarp + 1) {
+      // ---- TMA warps: items, Q and K; V ---------------------------------------------
+      const bool isV = warp != kChTmaWarp;
+      const CUtensorMap *map = isV ? &mapV : &mapK;
       const int per_head = a.seqs[a.B].base;
       const long long total = (long long)per_head * a.Hkv;
-      const int nfrag = kChKeys / frag_rows, per = 32 / nfrag;
-      int slot = 0, unit = 0, q_count = 0;
+      const int nparts = kChKeys / tl.part, per = 32 / nparts;
+      int slot = isV, unit = 0, q_count = 0;  // K and V take the ring's slots in turn
       uint32_t phase = 0;
       bool alive = true;
       for (int it = 0; alive; ++it) {
-        uint32_t x = 0;
-        if (lane == 0) x = atomicAdd(&a.head->next, 1u);
-        x = __shfl_sync(0xffffffffu, x, 0);
         ChItem &I = sm->item[it & 1];
-        if (!__all_sync(0xffffffffu,
-                        ch_wait(&sm->item_empty[it & 1], ((it >> 1) & 1) ^ 1, sm, a.status)))
-          break;
-        const bool valid = x < total;
-        if (valid) {
-          const int y = (int)(x % (uint32_t)per_head);
-          PgSeq sq;
-          const int b = pg_find(a.seqs, a.B, y, &sq);
+        if (isV) {
+          if (!__all_sync(0xffffffffu,
+                          ch_wait(&sm->item_full[it & 1], (it >> 1) & 1, sm, a.status)))
+            break;
+        } else {
+          uint32_t x = 0;
+          if (lane == 0) x = atomicAdd(&a.head->next, 1u);
+          x = __shfl_sync(0xffffffffu, x, 0);
+          if (!__all_sync(0xffffffffu,
+                          ch_wait(&sm->item_empty[it & 1], ((it >> 1) & 1) ^ 1, sm, a.status)))
+            break;
+          const bool valid = x < total;
+          if (valid) {
+            const int y = (int)(x % (uint32_t)per_head);
+            PgSeq sq;
+            const int b = pg_find(a.seqs, a.B, y, &sq);
+            if (lane == 0) {
+              int row0, n, kv;
+              pg_lengths(a, b, &row0, &n, &kv);
+              const int nrb = (n + TB - 1) / TB;
+              // piece-major, the blocks with the longest ranges first
+              const int piece = (y - sq.base) / nrb, rb = nrb - 1 - (y - sq.base) % nrb;
+              const int t0 = rb * TB, t1 = min(n, t0 + TB);
+              const int p_first = kv - n + t0, p_last = kv - n + t1 - 1;
+              const PgTiles t = pg_tiles(p_first, p_last, a.window, a.sinks, kChKeys);
+              I.b = b;
+              I.h = (int)(x / (uint32_t)per_head);
+              I.row0 = row0;
+              I.t0 = t0;
+              I.rows = (t1 - t0) * G;
+              I.p_first = p_first;
+              I.p_last = p_last;
+              I.low = pg_window_low(p_first, a.window);
+              I.sink_tiles = t.sink_tiles;
+              I.lo = t.lo;
+              I.u0 = min(piece * sq.len, t.units());
+              I.u1 = min(t.units(), I.u0 + sq.len);
+              I.np = sq.np;
+              I.piece = piece;
+              I.first = sq.slot + rb * sq.np;
+            }
+          }
           if (lane == 0) {
-            int row0, n, kv;
-            pg_lengths(a, b, &row0, &n, &kv);
-            const int nrb = (n + TB - 1) / TB;
-            // piece-major, the blocks with the longest ranges first
-            const int piece = (y - sq.base) / nrb, rb = nrb - 1 - (y - sq.base) % nrb;
-            const int t0 = rb * TB, t1 = min(n, t0 + TB);
-            const int p_first = kv - n + t0, p_last = kv - n + t1 - 1;
-            const PgTiles t = pg_tiles(p_first, p_last, a.window, a.sinks, kChKeys);
-            I.b = b;
-            I.h = (int)(x / (uint32_t)per_head);
-            I.row0 = row0;
-            I.t0 = t0;
-            I.rows = (t1 - t0) * G;
-            I.p_first = p_first;
-            I.p_last = p_last;
-            I.low = pg_window_low(p_first, a.window);
-            I.sink_tiles = t.sink_tiles;
-            I.lo = t.lo;
-            I.u0 = min(piece * sq.len, t.units());
-            I.u1 = min(t.units(), I.u0 + sq.len);
-            I.np = sq.np;
-            I.piece = piece;
-            I.first = sq.slot + rb * sq.np;
+            I.valid = valid;
+            mbar_arrive(&sm->item_full[it & 1]);
           }
+          __syncwarp();
         }
-        if (lane == 0) {
-          I.valid = valid;
-          mbar_arrive(&sm->item_full[it & 1]);
-        }
+        const int valid = I.valid, u0 = I.u0, u1 = I.u1, h = I.h, low = I.low;
+        const int limit = I.p_last + 1, sink_tiles = I.sink_tiles, lo = I.lo, b = I.b;
+        const int rows = I.rows, q_row = I.row0 + I.t0;
         __syncwarp();
+        if (isV && lane == 0) mbar_arrive(&sm->item_empty[it & 1]);
         if (!valid) break;
-        const int u0 = I.u0, u1 = I.u1, h = I.h, low = I.low, limit = I.p_last + 1;
-        const int sink_tiles = I.sink_tiles, lo = I.lo;
         if (u0 >= u1) continue;
-        // Q: the block's one or two row tiles
-        if (!__all_sync(0xffffffffu, ch_wait(&sm->q_empty, (q_count & 1) ^ 1, sm, a.status))) break;
-        ++q_count;
-        if (lane == 0) {
-          const int tiles = I.rows > TPT * G ? 2 : 1;
-          mbar_arrive_expect_tx(&sm->q_full, tiles * C::CB * TPT * G * 128);
-          for (int t = 0; t < tiles; ++t)
-            for (int c = 0; c < C::CB; ++c)
-              ch_tma(base + C::kQOff + t * C::kQTile + c * (128 * 128), &mapQ, c * 64, h * G,
-                     I.row0 + I.t0 + t * TPT, &sm->q_full);
+        if (!isV) {  // Q: the block's one or two row tiles
+          if (!__all_sync(0xffffffffu, ch_wait(&sm->q_empty, (q_count & 1) ^ 1, sm, a.status)))
+            break;
+          ++q_count;
+          if (lane == 0) {
+            const int tiles = rows > TPT * G ? 2 : 1;
+            mbar_arrive_expect_tx(&sm->q_full, tiles * C::CB * TPT * G * 128);
+            for (int t = 0; t < tiles; ++t)
+              for (int c = 0; c < C::CB; ++c)
+                ch_tma(base + C::kQOff + t * C::kQTile + c * (128 * 128), &mapQ, c * 64, h * G,
+                       q_row + t * TPT, &sm->q_full);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        const int *table = a.table + (size_t)I.b * a.blocks;
-        auto key_of = [&](int u) {
-          return (u < sink_tiles ? u : u - sink_tiles + lo) * kChKeys;
-        };
-        // lane i: table entry of fragment i % nfrag of tile ub + i / nfrag; -1: not read
+        const int *table = a.table + (size_t)b * a.blocks;
+        // lane i: where part i % nparts of tile ub + i / nparts is (token of its
+        // page, page * Hkv + head); past the pool (zeros) if it is not read
+        int y, z;
+        bool bad;
         auto fetch = [&](int ub) {
-          const int u = ub + lane / nfrag;
-          int e = -1;
-          if (lane < per * nfrag && u < u1) {
-            const int j0 = key_of(u) + (lane % nfrag) * frag_rows;
-            if (j0 < limit && (j0 + frag_rows > low || j0 < a.sinks)) {
-              e = table[j0 / a.page];
-              if (e < 0 || e >= a.pages) {
-                raise_flag(a.status, FLAG_INDEX);
-                e = -2;
+          const int u = ub + lane / nparts;
+          int yy = 0, zz = a.pages * a.Hkv;
+          bool bb = false;
+          if (u < u1) {
+            const int j0 = (u < sink_tiles ? u : u - sink_tiles + lo) * kChKeys +
+                           (lane % nparts) * tl.part;
+            if (j0 < limit && (j0 + tl.part > low || j0 < a.sinks)) {
+              const int blk = (int)((uint32_t)j0 / (uint32_t)a.page), e = table[blk];
+              if (e >= 0 && e < a.pages) {
+                yy = j0 - blk * a.page;
+                zz = e * a.Hkv + h;
+              } else {
+                if (isV) raise_flag(a.status, FLAG_INDEX);
+                bb = true;
               }
             }
           }
-          return e;
+          y = yy;
+          z = zz;
+          bad = bb;
         };
-        int next = fetch(u0);
+        fetch(u0);
         for (int ub = u0; ub < u1 && alive; ub += per) {
-          const int cur = next;
-          next = fetch(ub + per);
-          for (int u = ub; u < min(u1, ub + per) && alive; ++u) {
-            const int e = __shfl_sync(0xffffffffu, cur, (u - ub) * nfrag + lane % nfrag);
-            const uint32_t bad = __ballot_sync(0xffffffffu, lane < nfrag && e == -2);
-            const int j0 = key_of(u) + (lane % nfrag) * frag_rows;
-            const int y = e >= 0 ? j0 % a.page : 0;
-            const int z = e >= 0 ? e * a.Hkv + h : a.pages * a.Hkv;  // past the pool: zeros
-            for (int kv = 0; kv < 2; ++kv) {
-              if (!__all_sync(0xffffffffu, ch_wait(&sm->empty[slot], phase ^ 1u, sm, a.status))) {
-                alive = false;
-                break;
-              }
-              if (lane == 0) {
-                if (kv == 0) {  // one bit per 16 keys
-                  uint32_t ok16 = 0;
-                  for (int i = 0; i < kChKeys / 16; ++i)
-                    ok16 |= (~(bad >> (i * 16 / frag_rows)) & 1u) << i;
-                  sm->ok[unit & 7] = ok16;
-                }
-                mbar_arrive_expect_tx(&sm->full[slot], C::kTile);
-              }
-              __syncwarp();
-              if (lane < nfrag) {
-                const uint32_t dst = base + C::kRingOff + slot * C::kTile + lane * frag_rows * 128;
-  #pragma unroll
-                for (int c = 0; c < C::CB; ++c)
-                  ch_tma(dst + c * (kChKeys * 128), kv ? &mapV : &mapK, c * 64, y, z,
-                         &sm->full[slot]);
-              }
-              __syncwarp();
-              if (++slot == C::kSlots) slot = 0, phase ^= 1u;
+          const int cy = y, cz = z;
+          const uint32_t cbad = __ballot_sync(0xffffffffu, bad);
+          fetch(ub + per);
+          for (int u = ub; u < min(u1, ub + per); ++u) {
+            const int src = (u - ub) * nparts + lane % nparts;
+            const int ty = __shfl_sync(0xffffffffu, cy, src);
+            const int tz = __shfl_sync(0xffffffffu, cz, src);
+            if (!__all_sync(0xffffffffu, ch_wait(&sm->empty[slot], phase ^ 1u, sm, a.status))) {
+              alive = false;
+              break;
             }
+            if (lane == 0) {
+              if (isV) {  // one bit per 16 keys; the softmax waits for V before it looks
+                uint32_t ok16 = 0;
+                const uint32_t bits = cbad >> ((u - ub) * nparts);
+                for (int i = 0; i < kChKeys / 16; ++i)
+                  ok16 |= (~(bits >> (i * 16 / tl.part)) & 1u) << i;
+                sm->ok[unit & 7] = ok16;
+              }
+              mbar_arrive_expect_tx(&sm->full[slot], C::kTile);
+            }
+            __syncwarp();
+            if (lane < nparts)
+              pg_tma_part(base + C::kRingOff + slot * C::kTile + lane * tl.part * (D * 2), map, tl,
+                          ty, tz, &sm->full[slot]);
+            __syncwarp();
+            slot += 2;
+            if (slot >= C::kSlots) slot -= C::kSlots, phase ^= 1u;
             ++unit;
           }
         }
       }
+      // this warp's copies have landed before it leaves, whatever happened (the
+      // last kSlots positions of the ring: an older slot has moved on)
+      for (int at = 2 * unit - 2 + isV; at >= max(0, 2 * unit - C::kSlots); at -= 2)
+        mbar_wait(&sm->full[at % C::kSlots], (at / C::kSlots) & 1, a.status);
     } else if (warp == kChMmaWarp) {
       // ---- MMA thread ------------------------------------------------------------------
       if (lane == 0) {
@@ -362,12 +379,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
         };
         auto issue_s = [&](int t, int kslot) {
           const uint64_t q = ch_desc(base + C::kQOff + t * C::kQTile, 16, 1024);
-          const uint64_t k = ch_desc(base + C::kRingOff + kslot * C::kTile, 16, 1024);
+          const uint64_t k = ch_desc(base + C::kRingOff + kslot * C::kTile, 16, tl.group);
+          const uint32_t kcol = tl.col / 16;
   #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
             // the address field of a descriptor counts 16-byte units
-            const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) / 16;
-            ch_mma_ss(tmem + t * 128, q + off, k + off, idS, s > 0);
+            ch_mma_ss(tmem + t * 128, q + ((s >> 2) * (128 * 128) + (s & 3) * 32) / 16,
+                      k + (s >> 2) * kcol + (s & 3) * 2, idS, s > 0);
           }
           ch_commit(&sm->s_full[t]);
         };
@@ -408,11 +426,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
               if (!ok) break;
               ch_fence_after();
               const uint64_t v =
-                  ch_desc(base + C::kRingOff + vslot * C::kTile, kChKeys * 128, 1024);
+                  ch_desc(base + C::kRingOff + vslot * C::kTile, tl.col, tl.group);
+              const uint32_t vstep = 2 * tl.group / 16;  // 16 keys
   #pragma unroll
               for (int kk = 0; kk < kChKeys / 16; ++kk)
                 ch_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
-                          v + kk * (2048 / 16), idPV, j > 0 || kk > 0);
+                          v + kk * vstep, idPV, j > 0 || kk > 0);
               ch_commit(&sm->pv_done[t]);
               ++pv_cnt[t];
               if (t == tiles - 1) ch_commit(&sm->empty[vslot]);
@@ -504,13 +523,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
           // V rows that no row of the block sees may hold anything: clear them
           const int key = key0 + r;
           if (key > I.p_last || (key < I.low && key >= a.sinks)) {
-            const uint32_t v = base + C::kRingOff + vslot * C::kTile + r * 128;
+            const uint32_t v =
+                base + C::kRingOff + vslot * C::kTile + (r >> 3) * tl.group + (r & 7) * 128;
 #pragma unroll
             for (int c = 0; c < C::CB; ++c)
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                 v + c * (kChKeys * 128) + i * 16),
+                                 v + c * tl.col + ((i + r) & 7) * 16),
                              "r"(0u)
                              : "memory");
           }
@@ -528,8 +548,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
           for (int w = 0; w < 4; ++w) {
             const uint32_t pages = ((good >> (2 * w)) & 1u ? 0xffffu : 0u) |
                                    ((good >> (2 * w)) & 2u ? 0xffff0000u : 0u);
-            const uint32_t see = ch_below(hi + 1 - 32 * w) &
-                                 (~ch_below(lo - 32 * w) | ch_below(sk - 32 * w)) & pages;
+            const uint32_t see = pg_below(hi + 1 - 32 * w) &
+                                 (~pg_below(lo - 32 * w) | pg_below(sk - 32 * w)) & pages;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (!((see >> i) & 1u)) s[w * 32 + i] = 0xff800000u;
@@ -690,12 +710,12 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   auto kern = paged_chunk_kernel<D>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int frag = pg_part_rows(s.page, s.blocks, kChKeys);
+  const PgTile tile = pg_tile(s.page, s.blocks, D, kChKeys);
   const int TPT = 128 / s.G();
   CUtensorMap mq, mk, mv;
   e = pg_query_map(&mq, a.q, D, s.Hq, s.T, a.q_stride, s.G(), TPT);
-  if (e == cudaSuccess) e = pg_cache_map(&mk, a.K, D, s.page, (long long)s.pages * s.Hkv, frag);
-  if (e == cudaSuccess) e = pg_cache_map(&mv, a.V, D, s.page, (long long)s.pages * s.Hkv, frag);
+  if (e == cudaSuccess) e = pg_cache_map(&mk, a.K, D, s.page, (long long)s.pages * s.Hkv, tile);
+  if (e == cudaSuccess) e = pg_cache_map(&mv, a.V, D, s.page, (long long)s.pages * s.Hkv, tile);
   if (e != cudaSuccess) return e;
   if ((e = launch_paged_schedule(s, a, 2 * TPT, kChKeys, di.sm_count, st)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -707,7 +727,7 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.numAttrs = 0;
   add_pdl_attr(cfg, attrs);
-  e = cudaLaunchKernelEx(&cfg, kern, a, mq, mk, mv, frag);
+  e = cudaLaunchKernelEx(&cfg, kern, a, mq, mk, mv, tile);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

@@ -9,14 +9,15 @@
 // partial (O, max, sum), and the last of the pair's runs to arrive merges them
 // in run order (so the result does not depend on which one that is).
 //
-// A CTA is one producer warp and four consumer warps.  The producer streams
-// the run's tiles through a ring of shared-memory stages with TMA (one copy
-// per page fragment and 64 columns, 128-byte swizzle), across pair
-// boundaries, so the ring never drains.  Each consumer warp takes 16 keys of a
-// tile with its own running maximum, sum and O: S = Q K^T and O += P V on
-// mma.sync m16n8k16 -- 16 rows are all there is, a quarter of the smallest
-// tcgen05 tile, and nothing has to leave the registers between the two
-// products.  P is split in two bf16 parts (P_hi + P_lo: 16 significant bits),
+// A CTA is two producer warps and four consumer warps.  The producers stream
+// the run's K and V tiles through a ring of shared-memory stages with TMA (one
+// copy per page and tile, 128-byte swizzle), across pair boundaries, so the
+// ring never drains.  Each consumer warp takes every fourth tile with its own
+// running maximum, sum and O: S = Q K^T and O += P V on mma.sync m16n8k16 --
+// 16 rows are all there is, a quarter of the smallest tcgen05 tile, and nothing
+// has to leave the registers between the two products.  (Sharing each tile
+// between the warps, 16 keys each, made a tile's chain of latencies the limit
+// at d = 64.)  P is split in two bf16 parts (P_hi + P_lo: 16 significant bits),
 // which costs nothing where memory is the limit.
 #include "paged.h"
 #include "paged.cuh"
@@ -26,93 +27,131 @@ namespace sd {
 namespace {
 
 constexpr int kDcKeys = 64;      // keys per tile
-constexpr int kDcWarps = 4;      // consumer warps, 16 keys each
-constexpr int kDcThreads = 32 * (kDcWarps + 1);
+constexpr int kDcWarps = 4;      // consumer warps
+constexpr int kDcThreads = 32 * (kDcWarps + 2);
 constexpr int kDcRows = 16;
-constexpr int kDcMinRun = 2;     // tiles a run has at least
+constexpr int kDcMerge = 8;      // partials merged at a time
+constexpr int kDcGroup = 16;     // runs of a pair merged at once
+static_assert(kPagedMaxRuns / kDcGroup <= kPagedTops, "a counter per stretch of kDcGroup runs");
 
 template <int D>
 struct DcCfg {
   static constexpr int kTile = kDcKeys * D * 2;           // K or V of a tile
-  static constexpr int kStages = D == 128 ? 5 : 10;
+  // a multiple of the consumer warps: a stage's tiles all belong to one warp,
+  // which has then seen every phase of the stage's barrier before the next (a
+  // parity wait is only sound one phase ahead)
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static_assert(kStages % kDcWarps == 0, "a stage belongs to one warp");
   static constexpr int kRing = kStages * 2 * kTile;
   static constexpr int kOS = D + 8;                        // floats between rows of O
   static constexpr int kOBytes = kDcWarps * kDcRows * kOS * 4;
   static constexpr int kSmem = kRing + kOBytes + 1024 + 1024;  // + small, alignment
 };
 
-// where a run starts: sequence, KV head, tile of the pair
+// a / b, by 32-bit division where both allow it
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// Where a run starts: sequence, KV head, tile of the pair.
 struct DcStart {
-  int b, h, u, pad;
-};
-struct DcHead {
-  long long total;  // tiles of the call
-  long long run;    // tiles per run
+  long long total, run;  // tiles of the call, tiles per run
+  int align;             // a pair's tiles are counted in multiples of this
+  int b, h, u;
 };
 
 __device__ __forceinline__ int dc_units(const PgTiles &t) { return max(t.units(), 1); }
+__device__ __forceinline__ int dc_round(int units, int align) {
+  return align == 1 ? units : (units + align - 1) / align * align;
+}
+// tiles of a (sequence, head) pair; 0: the sequence has no new tokens
+__device__ __forceinline__ int dc_pair(const PgArgs &a, int b, bool report) {
+  int row0, n, kv;
+  if (!pg_lengths(a, b, &row0, &n, &kv)) {
+    if (report) raise_flag(a.status, FLAG_INDEX);
+    return 0;
+  }
+  return n == 0 ? 0 : dc_units(pg_tiles(kv - n, kv - 1, a.window, a.sinks, kDcKeys));
+}
 
-__global__ void __launch_bounds__(1024) paged_decode_schedule_kernel(const PgArgs a, int workers) {
-  __shared__ long long s_pre[kPagedMaxB + 1];
-  __shared__ long long s_w[32], s_carry;
+// Runs are equal shares of the call's tiles, which balances any batch, unless
+// whole multiples of 4, 8 or 16 tiles of single pairs fit the grid: a small
+// call is a matter of latency, and runs that never cross a pair then have
+// fewer steps one after another (one token each over eight heads of 16 tokens:
+// 26 us in runs of four pairs).
+constexpr int kDcAligns = 4;  // 1, 4, 8, 16: 1 or 2 << i
+
+// Every CTA finds its own run: thread i sums a stretch of the batch, a block
+// scan gives the total and the stretch's first tile, and the thread whose
+// stretch holds the run's first tile walks to it.  (A kernel of its own for
+// this cost a launch and 4 us of a one-request call.)
+__device__ __forceinline__ void dc_schedule(const PgArgs &a, DcStart *st,
+                                            long long (*sums)[kDcAligns]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_dep_wait();
-  grid_dep_launch();
-  if (tid == 0) s_carry = 0;
-  __syncthreads();
-  for (int b0 = 0; b0 < a.B; b0 += 1024) {
-    const int b = b0 + tid;
-    long long u = 0;
-    if (b < a.B) {
-      int row0, n, kv;
-      if (!pg_lengths(a, b, &row0, &n, &kv)) raise_flag(a.status, FLAG_INDEX);
-      else if (n > 0)
-        u = (long long)a.Hkv * dc_units(pg_tiles(kv - n, kv - 1, a.window, a.sinks, kDcKeys));
-    }
-    long long x = u;
+  const int per = (a.B + kDcThreads - 1) / kDcThreads;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  long long mine[kDcAligns] = {}, x[kDcAligns];
+  for (int b = b0; b < b1; ++b) {
+    const int u = dc_pair(a, b, blockIdx.x == 0);
+#pragma unroll
+    for (int i = 0; i < kDcAligns; ++i)
+      mine[i] += (long long)a.Hkv * dc_round(u, i == 0 ? 1 : 2 << i);
+  }
+#pragma unroll
+  for (int i = 0; i < kDcAligns; ++i) {
+    x[i] = mine[i];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long p = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += p;
+      const long long p = __shfl_up_sync(0xffffffffu, x[i], o);
+      if (lane >= o) x[i] += p;
     }
-    if (lane == 31) s_w[warp] = x;
-    __syncthreads();
-    long long base = s_carry;
-    for (int w = 0; w < warp; ++w) base += s_w[w];
-    if (b < a.B) s_pre[b] = base + x - u;
-    __syncthreads();
-    if (tid == 1023) s_carry = base + x;
-    __syncthreads();
+    if (lane == 31) sums[warp][i] = x[i];
   }
-  const long long total = s_carry;
-  long long run = (total + workers - 1) / workers;
-  if (run < kDcMinRun) run = kDcMinRun;
-  DcHead *hd = reinterpret_cast<DcHead *>(a.head);
-  if (tid == 0) {
-    s_pre[a.B] = total;
-    *hd = DcHead{total, run};
-  }
-  DcStart *st = reinterpret_cast<DcStart *>(a.seqs);
-  for (int w = tid; w < workers; w += 1024) {
-    const long long x = w * run;
-    if (x < total) {
-      int lo = 0, hi = a.B - 1;  // the last sequence whose tiles start at or before x
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_pre[mid] <= x) lo = mid;
-        else hi = mid - 1;
+  __syncthreads();
+  int pick = 0;
+  long long total = 0, run = 0, base = 0, part = 0;
+#pragma unroll
+  for (int i = kDcAligns - 1; i >= 0; --i) {
+    long long t = 0, bs = x[i] - mine[i];
+#pragma unroll
+    for (int w = 0; w < kDcThreads / 32; ++w) {
+      if (w < warp) bs += sums[w][i];
+      t += sums[w][i];
+    }
+    const int al = 2 << i;
+    if (i == 0 || t <= (long long)gridDim.x * al) {
+      if (i > 0 || pick == 0) {
+        pick = i;
+        total = t;
+        base = bs;
+        part = mine[i];
+        run = i > 0 ? al : div_ll(t + gridDim.x - 1, gridDim.x);
       }
-      const long long end = lo + 1 < a.B ? s_pre[lo + 1] : total;
-      const long long per = (end - s_pre[lo]) / a.Hkv, off = x - s_pre[lo];
-      st[w] = DcStart{lo, (int)(off / per), (int)(off % per), 0};
     }
-    a.arrive[w] = 0u;
   }
+  const int align = pick > 0 ? 2 << pick : 1;
+  const long long x0 = (long long)blockIdx.x * run;
+  if (tid == 0) st->total = total, st->run = run, st->align = align;
+  if (part > 0 && base <= x0 && x0 < base + part) {
+    for (int b = b0; b < b1; ++b) {
+      const int each = dc_round(dc_pair(a, b, false), align);
+      const long long t = (long long)a.Hkv * each;
+      if (x0 < base + t) {
+        const long long off = x0 - base;
+        st->b = b;
+        st->h = (int)div_ll(off, each);
+        st->u = (int)(off - (long long)st->h * each);
+        break;
+      }
+      base += t;
+    }
+  }
+  __syncthreads();
 }
 
 // One (sequence, KV head) pair's part of a run.
 struct DcSeg {
-  int b, h, row0, n, kv, units, u0, u1;
+  int b, h, row0, n, kv, units, u0, u1;  // units: rounded up where runs are aligned
+  bool cut;                              // not the whole pair
   int p_first, limit, low;  // first row's position; keys the rows see: j < limit and (j >= low or a sink)
   PgTiles t;
 };
@@ -120,7 +159,7 @@ struct DcSeg {
 // Walks a run's segments: every warp of the CTA takes the same walk.
 struct DcWalk {
   long long left, item;  // tiles left in the run; the pair's first tile in the call's list
-  int b, h, u;
+  int b, h, u, align;
   __device__ bool next(const PgArgs &a, DcSeg *s) {
     if (left <= 0) return false;
     int row0, n, kv;
@@ -136,10 +175,13 @@ struct DcWalk {
     s->limit = kv;
     s->low = pg_window_low(kv - n, a.window);
     s->t = pg_tiles(kv - n, kv - 1, a.window, a.sinks, kDcKeys);
-    s->units = dc_units(s->t);
+    const int units = dc_units(s->t);
+    s->units = dc_round(units, align);
     s->u0 = u;
-    s->u1 = (int)min((long long)s->units, u + left);
-    left -= s->u1 - u;
+    const int end = (int)min((long long)s->units, u + left);
+    left -= end - u;
+    s->cut = end - u < s->units;
+    s->u1 = min(end, units);
     return true;
   }
   // past the segment just taken
@@ -172,14 +214,6 @@ __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
-                                     uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
@@ -191,9 +225,8 @@ __device__ __forceinline__ void consumers_sync() {
 template <int D>
 __global__ void __launch_bounds__(kDcThreads, 1)
     paged_decode_kernel(const PgArgs a, const __grid_constant__ CUtensorMap mapK,
-                        const __grid_constant__ CUtensorMap mapV, int part_rows) {
+                        const __grid_constant__ CUtensorMap mapV, const PgTile tl) {
   using C = DcCfg<D>;
-  constexpr int CB = D / 64;  // 64-column blocks of a row
   extern __shared__ unsigned char raw[];
   const uint32_t raw_s = smem_u32(raw);
   const uint32_t base = (raw_s + 1023u) & ~1023u;
@@ -205,83 +238,98 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   uint32_t *okmask = reinterpret_cast<uint32_t *>(empty + C::kStages);
   float *ml = reinterpret_cast<float *>(okmask + C::kStages);     // [warp][row][2]
   uint32_t *flag = reinterpret_cast<uint32_t *>(ml + kDcWarps * kDcRows * 2);
+  __shared__ DcStart s0;
+  __shared__ long long warp_sums[kDcThreads / 32][kDcAligns];
   static_assert(C::kStages * 20 + kDcWarps * kDcRows * 8 + 4 <= 1024, "small area");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kDcWarps);
+      mbar_init(&full[i], 2);   // K and V
+      mbar_init(&empty[i], 1);  // the warp that takes the tile
     }
     fence_mbar_init();
+    pg_prefetch_map(&mapK);
+    pg_prefetch_map(&mapV);
   }
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
-  const DcHead hd = *reinterpret_cast<const DcHead *>(a.head);
-  const long long x0 = (long long)blockIdx.x * hd.run;
-  if (x0 >= hd.total) return;
-  const DcStart s0 = reinterpret_cast<const DcStart *>(a.seqs)[blockIdx.x];
-  DcWalk walk{min(hd.run, hd.total - x0), x0 - s0.u, s0.b, s0.h, s0.u};
+  dc_schedule(a, &s0, warp_sums);
+  const long long run = s0.run, x0 = (long long)blockIdx.x * run;
+  if (x0 >= s0.total) return;
+  DcWalk walk{min(run, s0.total - x0), x0 - s0.u, s0.b, s0.h, s0.u, s0.align};
   DcSeg seg;
-  const int page = a.page;
-  const int nparts = kDcKeys / part_rows;
+  const int page = a.page, part_rows = tl.part;
+  const int nparts = kDcKeys / part_rows, part_log = 31 - __clz(part_rows);
 
-  if (warp == kDcWarps) {
-    // ---- producer ------------------------------------------------------------
+  if (warp >= kDcWarps) {
+    // ---- producers: K, V ----------------------------------------------------------
+    const bool isV = warp > kDcWarps;
+    const CUtensorMap *map = isV ? &mapV : &mapK;
     const int per = 32 / nparts;  // tiles whose table entries the lanes hold
-    int stage = 0;
+    int stage = 0, issued = 0;
     uint32_t phase = 0;
-    while (walk.next(a, &seg)) {
+    bool alive = true;
+    while (alive && walk.next(a, &seg)) {
       const int *table = a.table + (size_t)seg.b * a.blocks;
-      // lane i: entry of part i % nparts of tile ub + i / nparts; -1: not read
+      // lane i: where part i % nparts of tile ub + i / nparts is (token of its
+      // page, page * Hkv + head); past the pool (zeros) if it is not read
+      int y, z;
+      bool bad;
       auto fetch = [&](int ub) {
         const int u = ub + lane / nparts;
-        int e = -1;
-        if (lane < per * nparts && u < seg.u1) {
+        int yy = 0, zz = a.pages * a.Hkv;
+        bool bb = false;
+        if (u < seg.u1) {
           const int j0 = seg.t.tile(u) * kDcKeys + (lane % nparts) * part_rows;
           // some row sees one of the part's keys
           if (j0 < seg.limit && (j0 + part_rows > seg.low || j0 < a.sinks)) {
-            e = table[j0 / page];
-            if (e < 0 || e >= a.pages) {
-              raise_flag(a.status, FLAG_INDEX);
-              e = -2;
+            const int blk = (int)((uint32_t)j0 / (uint32_t)page), e = table[blk];
+            if (e >= 0 && e < a.pages) {
+              yy = j0 - blk * page;
+              zz = e * a.Hkv + seg.h;
+            } else {
+              if (!isV) raise_flag(a.status, FLAG_INDEX);
+              bb = true;
             }
           }
         }
-        return e;
+        y = yy;
+        z = zz;
+        bad = bb;
       };
-      int next = fetch(seg.u0);
-      for (int ub = seg.u0; ub < seg.u1; ub += per) {
-        const int cur = next;
-        next = fetch(ub + per);
+      fetch(seg.u0);
+      for (int ub = seg.u0; ub < seg.u1 && alive; ub += per) {
+        const int cy = y, cz = z;
+        const uint32_t cbad = __ballot_sync(0xffffffffu, bad);
+        fetch(ub + per);
         for (int u = ub; u < min(seg.u1, ub + per); ++u) {
-          const int e = __shfl_sync(0xffffffffu, cur, (u - ub) * nparts + lane % nparts);
-          const uint32_t bad = __ballot_sync(0xffffffffu, lane < nparts && e == -2);
-          if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, a.status))) return;
+          const int src = (u - ub) * nparts + lane % nparts;
+          const int ty = __shfl_sync(0xffffffffu, cy, src);
+          const int tz = __shfl_sync(0xffffffffu, cz, src);
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, a.status))) {
+            alive = false;
+            break;
+          }
           if (lane == 0) {
-            okmask[stage] = ~bad;
-            mbar_arrive_expect_tx(&full[stage], 2 * C::kTile);
+            if (!isV) okmask[stage] = ~(cbad >> ((u - ub) * nparts));
+            mbar_arrive_expect_tx(&full[stage], C::kTile);
           }
           __syncwarp();
-          if (lane < nparts) {
-            const int j0 = seg.t.tile(u) * kDcKeys + lane * part_rows;
-            const int y = e >= 0 ? j0 % page : 0;
-            const int z = e >= 0 ? e * a.Hkv + seg.h : a.pages * a.Hkv;  // past the pool: zeros
-            const uint32_t k = base + stage * 2 * C::kTile + lane * part_rows * 128;
-#pragma unroll
-            for (int c = 0; c < CB; ++c)
-              tma3(k + c * (kDcKeys * 128), &mapK, c * 64, y, z, &full[stage]);
-#pragma unroll
-            for (int c = 0; c < CB; ++c)
-              tma3(k + C::kTile + c * (kDcKeys * 128), &mapV, c * 64, y, z, &full[stage]);
-          }
+          if (lane < nparts)
+            pg_tma_part(base + (2 * stage + isV) * C::kTile + lane * part_rows * (D * 2), map, tl,
+                        ty, tz, &full[stage]);
           __syncwarp();
           if (++stage == C::kStages) stage = 0, phase ^= 1u;
+          ++issued;
         }
       }
       walk.advance(a, seg);
     }
+    // this warp's copies have landed before it leaves, whatever happened
+    for (int i = max(0, issued - C::kStages); i < issued; ++i)
+      mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, a.status);
     return;
   }
 
@@ -290,7 +338,9 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
   __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
   const int g8 = lane >> 2, t4 = lane & 3;
-  int stage = 0;
+  // this warp's next tile of the run, and its stage
+  long long mine = warp, seg0 = 0;
+  int stage = warp;
   uint32_t phase = 0;
   bool dead = false;  // a wait ran out: no further waiting, the results are void
   while (walk.next(a, &seg)) {
@@ -319,69 +369,85 @@ __global__ void __launch_bounds__(kDcThreads, 1)
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    for (int u = seg.u0; u < seg.u1; ++u) {
-      const int key0 = seg.t.tile(u) * kDcKeys;
+    const long long seg1 = seg0 + seg.u1 - seg.u0;
+    for (; mine < seg1; mine += kDcWarps) {
+      const int key0 = seg.t.tile(seg.u0 + (int)(mine - seg0)) * kDcKeys;
       if (!dead && !mbar_wait(&full[stage], phase, a.status)) dead = true;
-      const uint32_t ok = okmask[stage];
+      const uint32_t all_parts = (1u << nparts) - 1u, ok = okmask[stage] & all_parts;
       const uint32_t ks = base + stage * 2 * C::kTile, vs = ks + C::kTile;
-      const bool bad_page = (ok & ((1u << nparts) - 1u)) != ((1u << nparts) - 1u);
       // every row sees every key of the tile
-      const bool whole = !bad_page && key0 + kDcKeys - 1 <= seg.p_first &&
+      const bool whole = ok == all_parts && key0 + kDcKeys - 1 <= seg.p_first &&
                          (key0 >= low_last || key0 + kDcKeys <= a.sinks);
       if (key0 + kDcKeys > seg.limit || (key0 < seg.low && key0 + kDcKeys > a.sinks)) {
-        // V rows that no row sees may hold anything: clear this warp's
-        const int r = warp * 16 + (lane >> 1), j = key0 + r;
-        if (j >= seg.limit || (j < seg.low && j >= a.sinks)) {
+        // V rows that no row sees may hold anything: clear them
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const int ch = (lane & 1) * (D / 16) + c;  // 16-byte piece; the swizzle permutes a row
-            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                             vs + (ch >> 3) * (kDcKeys * 128) + r * 128 + (ch & 7) * 16),
-                         "r"(0u)
-                         : "memory");
+        for (int i = 0; i < kDcKeys / 32; ++i) {
+          const int r = i * 32 + lane, j = key0 + r;
+          if (j >= seg.limit || (j < seg.low && j >= a.sinks)) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)  // 16-byte pieces, rotated: lanes hit other banks
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                               vs + (r >> 3) * tl.group + (c >> 3) * tl.col + (r & 7) * 128 +
+                               ((c + lane) & 7) * 16),
+                           "r"(0u)
+                           : "memory");
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
       }
-      float sc[2][4];
+      float sc[kDcKeys / 8][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+      for (int i = 0; i < kDcKeys / 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
       {
-        const int r = warp * 16 + ((lane >> 4) << 3) + (lane & 7);
-        const uint32_t row = ks + r * 128;
+        const uint32_t row = ks + (lane >> 4) * tl.group + (lane & 7) * 128;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           const int ch = 2 * s + ((lane >> 3) & 1);
-          uint32_t kf[4];
-          ldsm4(row + (ch >> 3) * (kDcKeys * 128) + (((ch & 7) ^ (r & 7)) << 4), kf);
-          mma16816(sc[0], qf[s], kf[0], kf[1]);
-          mma16816(sc[1], qf[s], kf[2], kf[3]);
+          const uint32_t at = row + (ch >> 3) * tl.col + (((ch & 7) ^ (lane & 7)) << 4);
+#pragma unroll
+          for (int kb = 0; kb < kDcKeys / 16; ++kb) {
+            uint32_t kf[4];
+            ldsm4(at + kb * 2 * tl.group, kf);
+            mma16816(sc[2 * kb], qf[s], kf[0], kf[1]);
+            mma16816(sc[2 * kb + 1], qf[s], kf[2], kf[3]);
+          }
         }
       }
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] *= a.scale_log2;
       if (!whole) {
+        // the keys a row sees, a bit each
+        uint32_t pages[2];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int w = 0; w < 2; ++w)
+          pages[w] = ((ok >> ((32 * w) >> part_log)) & 1u ? 0xffffu : 0u) |
+                     ((ok >> ((32 * w + 16) >> part_log)) & 1u ? 0xffff0000u : 0u);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = warp * 16 + nt * 8 + t4 * 2 + (e & 1), j = key0 + r;
-            const bool see = j <= pos[e >> 1] && (j >= low[e >> 1] || j < a.sinks) &&
-                             ((ok >> (r / part_rows)) & 1u);
-            if (!see) sc[nt][e] = -INFINITY;
+        for (int i = 0; i < 2; ++i) {
+          const int hi = pos[i] - key0, lo = low[i] - key0, sk = a.sinks - key0;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            uint32_t see = pg_below(hi + 1 - 32 * w) &
+                           (~pg_below(lo - 32 * w) | pg_below(sk - 32 * w)) & pages[w];
+            see >>= t4 * 2;
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!((see >> (nt * 8 + e)) & 1u)) sc[4 * w + nt][2 * i + e] = -INFINITY;
           }
+        }
       }
       float mx[2], use[2];
       bool up = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
+        mx[i] = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < kDcKeys / 8; ++nt)
+          mx[i] = fmaxf(mx[i], fmaxf(sc[nt][2 * i], sc[nt][2 * i + 1]));
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        mx[i] = fmaxf(mx[i], m[i]);
+        mx[i] = fmaxf(mx[i] * a.scale_log2, m[i]);
         use[i] = mx[i] == -INFINITY ? 0.f : mx[i];
         up |= mx[i] > m[i];
       }
@@ -399,26 +465,29 @@ __global__ void __launch_bounds__(kDcThreads, 1)
         m[0] = mx[0];
         m[1] = mx[1];
       }
-      uint32_t ph[4], pl[4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int kb = 0; kb < kDcKeys / 16; ++kb) {
+        uint32_t ph[4], pl[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float p0 = pg_exp2(sc[nt][2 * i] - use[i]), p1 = pg_exp2(sc[nt][2 * i + 1] - use[i]);
-          l[i] += p0 + p1;
-          const uint32_t hi = pack2(p0, p1);
-          ph[nt * 2 + i] = hi;
-          pl[nt * 2 + i] = pack2(p0 - __uint_as_float(hi << 16),
-                                 p1 - __uint_as_float(hi & 0xffff0000u));
-        }
-      {
-        const int r = warp * 16 + (lane & 15);
-        const uint32_t row = vs + r * 128;
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float *x = &sc[2 * kb + nt][2 * i];
+            const float p0 = pg_exp2(fmaf(x[0], a.scale_log2, -use[i]));
+            const float p1 = pg_exp2(fmaf(x[1], a.scale_log2, -use[i]));
+            l[i] += p0 + p1;
+            const uint32_t hi = pack2(p0, p1);
+            ph[nt * 2 + i] = hi;
+            pl[nt * 2 + i] = pack2(p0 - __uint_as_float(hi << 16),
+                                   p1 - __uint_as_float(hi & 0xffff0000u));
+          }
+        const uint32_t row =
+            vs + (2 * kb + ((lane >> 3) & 1)) * tl.group + (lane & 7) * 128;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           const int ch = 2 * s + (lane >> 4);
           uint32_t vf[4];
-          ldsm4t(row + (ch >> 3) * (kDcKeys * 128) + (((ch & 7) ^ (r & 7)) << 4), vf);
+          ldsm4t(row + (ch >> 3) * tl.col + (((ch & 7) ^ (lane & 7)) << 4), vf);
           mma16816(o[2 * s], ph, vf[0], vf[1]);
           mma16816(o[2 * s + 1], ph, vf[2], vf[3]);
           mma16816(o[2 * s], pl, vf[0], vf[1]);
@@ -427,8 +496,10 @@ __global__ void __launch_bounds__(kDcThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stage]);
-      if (++stage == C::kStages) stage = 0, phase ^= 1u;
+      stage += kDcWarps;
+      if (stage >= C::kStages) stage -= C::kStages, phase ^= 1u;
     }
+    seg0 = seg1;
 
     // ---- the four warps' parts of the segment, joined in shared memory ---------
 #pragma unroll
@@ -446,9 +517,9 @@ __global__ void __launch_bounds__(kDcThreads, 1)
         *reinterpret_cast<float2 *>(dst + c * 8) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
     }
     consumers_sync();
-    const bool cut = seg.u1 - seg.u0 < seg.units;
-    const int first = (int)(walk.item / hd.run);  // the pair's first and last run
-    const int last_run = (int)((walk.item + seg.units - 1) / hd.run);
+    // the pair's first and last run
+    const int first = (int)div_ll(walk.item, run);
+    const int last_run = (int)div_ll(walk.item + seg.units - 1, run);
     const size_t per = (size_t)a.part_rows * D;
     float2 *pml = reinterpret_cast<float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
     const size_t slot = 2 * (size_t)blockIdx.x + (seg.u0 == 0 ? 1 : 0);
@@ -481,44 +552,96 @@ __global__ void __launch_bounds__(kDcThreads, 1)
         acc.z += v.z * f;
         acc.w += v.w * f;
       }
-      if (!cut) {
+      if (!seg.cut) {
         store(r, c, acc, mm, ll);
       } else {
         *reinterpret_cast<float4 *>(a.part + slot * per + (size_t)r * D + c * 4) = acc;
         if (c == 0) pml[slot * a.part_rows + r] = make_float2(mm, ll);
       }
     }
-    if (cut) {
-      __threadfence();
-      consumers_sync();
-      if (tid == 0) *flag = atomicAdd(&a.arrive[first], 1u) == (uint32_t)(last_run - first);
-      consumers_sync();
-      if (*flag) {
-        // this was the pair's last run to arrive: merge all of them, in order
+    if (seg.cut) {
+      // Partials are merged by the last run to arrive, in run order; of more
+      // than kDcGroup runs by groups first (each group's last to arrive), then
+      // the groups: no one CTA reads them all.  A counter wraps to zero with
+      // the last arrival, so the counters stay clear between calls.
+      auto arrive_last = [&](uint32_t *ctr, int count) {
         __threadfence();
-        for (int i = tid; i < rows * (D / 4); i += 32 * kDcWarps) {
+        consumers_sync();
+        if (tid == 0) *flag = atomicInc(ctr, (uint32_t)count - 1) == (uint32_t)count - 1;
+        consumers_sync();
+        const bool l = *flag != 0;
+        if (l) __threadfence();
+        return l;
+      };
+      // merges the partials of runs w0, w0 + step, .. (n of them); the result
+      // is the pair's output, or replaces the first one
+      auto merge = [&](int w0, int step, int n, bool final) {
+        for (int i = tid; i < kDcRows * (D / 4); i += 32 * kDcWarps) {
           const int r = i / (D / 4), c = i % (D / 4);
-          float mm = -INFINITY;
-#pragma unroll 8
-          for (int w = first; w <= last_run; ++w)
-            mm = fmaxf(mm, __ldcg(&pml[(2 * (size_t)w + (w == first)) * a.part_rows + r].x));
-          const float us = mm == -INFINITY ? 0.f : mm;
+          if (r >= rows) break;
+          float mm = -INFINITY, ll = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float ll = 0.f;
-#pragma unroll 8
-          for (int w = first; w <= last_run; ++w) {
-            const size_t s = 2 * (size_t)w + (w == first);
-            const float2 e = __ldcg(&pml[s * a.part_rows + r]);
-            const float4 v = __ldcg(
-                reinterpret_cast<const float4 *>(a.part + s * per + (size_t)r * D + c * 4));
-            const float f = exp2f(e.x - us);
-            ll += e.y * f;
-            acc.x += v.x * f;
-            acc.y += v.y * f;
-            acc.z += v.z * f;
-            acc.w += v.w * f;
+          for (int k = 0; k < n; k += kDcMerge) {
+            // several at a time, all loads in flight together
+            float2 e[kDcMerge];
+            float4 v[kDcMerge];
+            float top = mm;
+#pragma unroll
+            for (int j = 0; j < kDcMerge; ++j) {
+              const int w = w0 + min(k + j, n - 1) * step;
+              const size_t s = 2 * (size_t)w + (w == first);
+              e[j] = __ldcg(&pml[s * a.part_rows + r]);
+              v[j] = __ldcg(
+                  reinterpret_cast<const float4 *>(a.part + s * per + (size_t)r * D + c * 4));
+              if (k + j >= n) e[j] = make_float2(-INFINITY, 0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < kDcMerge; ++j) top = fmaxf(top, e[j].x);
+            const float us = top == -INFINITY ? 0.f : top, corr = exp2f(mm - us);
+            mm = top;
+            ll *= corr;
+            acc.x *= corr;
+            acc.y *= corr;
+            acc.z *= corr;
+            acc.w *= corr;
+#pragma unroll
+            for (int j = 0; j < kDcMerge; ++j) {
+              const float f = exp2f(e[j].x - us);
+              ll += e[j].y * f;
+              acc.x += v[j].x * f;
+              acc.y += v[j].y * f;
+              acc.z += v[j].z * f;
+              acc.w += v[j].w * f;
+            }
           }
-          store(r, c, acc, mm, ll);
+          if (final) {
+            store(r, c, acc, mm, ll);
+          } else {
+            // every reader of this element of the first partial is this thread,
+            // but its (max, sum) has D / 4 readers: they meet below
+            const size_t s = 2 * (size_t)w0 + (w0 == first);
+            *reinterpret_cast<float4 *>(a.part + s * per + (size_t)r * D + c * 4) = acc;
+            if (c == 0) ml[r * 2] = mm, ml[r * 2 + 1] = ll;
+          }
+        }
+        if (!final) {
+          consumers_sync();
+          const size_t s = 2 * (size_t)w0 + (w0 == first);
+          if (tid < rows) pml[s * a.part_rows + tid] = make_float2(ml[tid * 2], ml[tid * 2 + 1]);
+        }
+      };
+      const int count = last_run - first + 1;
+      if (count <= kDcGroup) {
+        if (arrive_last(&a.runs[first], count)) merge(first, 1, count, true);
+      } else {
+        const int g = ((int)blockIdx.x - first) / kDcGroup, w0 = first + g * kDcGroup;
+        const int n = min(kDcGroup, count - g * kDcGroup);
+        // (a group's first run may be the next pair's first: other counters)
+        if (arrive_last(g == 0 ? &a.runs[w0] : &a.groups[w0], n)) {
+          merge(w0, 1, n, false);
+          const int groups = (count + kDcGroup - 1) / kDcGroup;
+          // pairs of more than kDcGroup runs start in different stretches of as many
+          if (arrive_last(&a.tops[first / kDcGroup], groups)) merge(first, kDcGroup, groups, true);
         }
       }
     }
@@ -536,28 +659,22 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   auto kern = paged_decode_kernel<D>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int part = pg_part_rows(s.page, s.blocks, kDcKeys);
+  const PgTile tile = pg_tile(s.page, s.blocks, D, kDcKeys);
   CUtensorMap mk, mv;
-  e = pg_cache_map(&mk, a.K, D, s.page, (long long)s.pages * s.Hkv, part);
-  if (e == cudaSuccess) e = pg_cache_map(&mv, a.V, D, s.page, (long long)s.pages * s.Hkv, part);
+  e = pg_cache_map(&mk, a.K, D, s.page, (long long)s.pages * s.Hkv, tile);
+  if (e == cudaSuccess) e = pg_cache_map(&mv, a.V, D, s.page, (long long)s.pages * s.Hkv, tile);
   if (e != cudaSuccess) return e;
   const int grid = di.sm_count < kPagedMaxRuns ? di.sm_count : kPagedMaxRuns;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attrs[1];
   cfg.stream = st;
   cfg.attrs = attrs;
-  cfg.gridDim = dim3(1, 1, 1);
-  cfg.blockDim = dim3(1024, 1, 1);
-  cfg.numAttrs = 0;
-  add_pdl_attr(cfg, attrs);
-  e = cudaLaunchKernelEx(&cfg, paged_decode_schedule_kernel, a, grid);
-  if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(kDcThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.numAttrs = 0;
   add_pdl_attr(cfg, attrs);
-  e = cudaLaunchKernelEx(&cfg, kern, a, mk, mv, part);
+  e = cudaLaunchKernelEx(&cfg, kern, a, mk, mv, tile);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

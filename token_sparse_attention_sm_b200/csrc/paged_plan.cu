@@ -21,7 +21,8 @@ namespace sd {
 namespace {
 
 constexpr int kPlThreads = 512;
-constexpr int kPlCluster = 8;
+constexpr int kPlCluster = 16;  // CTAs of the largest cluster (opt-in size)
+constexpr int kPlRows = 4;      // rows a thread has in flight
 
 struct PlanArgs {
   const int *new_lens, *lens, *free_pages, *free_count;
@@ -121,26 +122,41 @@ __global__ void __launch_bounds__(kPlThreads) paged_plan_kernel(const PlanArgs a
     const int old = (int)(((long long)past[b] + a.page - 1) / a.page);
     a.table[(size_t)b * a.blocks + old + i - take[b]] = taken(i);
   }
-  for (int t = t0; t < a.T; t += step) {
-    int pos = -1, slot = -1;
-    if (t < sum_rows) {
-      const int b = find_seq(rows, a.B, t);
-      pos = past[b] + t - rows[b];
-      const int blk = pos / a.page, old = (int)(((long long)past[b] + a.page - 1) / a.page);
-      int pg;
-      if (blk < old) {
-        pg = a.table[(size_t)b * a.blocks + blk];
-        if (pg < 0 || pg >= a.pages) {
-          raise_flag(a.status, FLAG_INDEX);
-          pg = -1;
-        }
-      } else {
-        pg = taken(take[b] + blk - old);
+  // four rows at a time, so that their searches and loads overlap
+  for (int tt = t0; tt < a.T; tt += kPlRows * step) {
+    int pos[kPlRows], slot[kPlRows];
+    const int *src[kPlRows];
+#pragma unroll
+    for (int i = 0; i < kPlRows; ++i) {
+      const int t = tt + i * step;
+      pos[i] = -1;
+      src[i] = nullptr;
+      if (t < sum_rows) {
+        const int b = find_seq(rows, a.B, t);
+        pos[i] = past[b] + t - rows[b];
+        const uint32_t blk = (uint32_t)pos[i] / a.page;
+        const uint32_t old = ((uint32_t)past[b] + a.page - 1) / a.page;
+        src[i] = blk < old ? a.table + (size_t)b * a.blocks + blk
+                           : a.free_pages + (fc - 1 - (take[b] + (int)(blk - old)));
       }
-      if (pg >= 0) slot = pg * a.page + pos % a.page;
     }
-    a.positions[t] = pos;
-    a.slots[t] = slot;
+#pragma unroll
+    for (int i = 0; i < kPlRows; ++i) slot[i] = src[i] ? *src[i] : -1;
+#pragma unroll
+    for (int i = 0; i < kPlRows; ++i) {
+      const int t = tt + i * step;
+      if (t >= a.T) break;
+      if (src[i]) {
+        if (slot[i] >= 0 && slot[i] < a.pages) {
+          slot[i] = slot[i] * a.page + (int)((uint32_t)pos[i] % a.page);
+        } else {
+          raise_flag(a.status, FLAG_INDEX);
+          slot[i] = -1;
+        }
+      }
+      a.positions[t] = pos[i];
+      a.slots[t] = slot[i];
+    }
   }
 }
 
@@ -156,6 +172,8 @@ cudaError_t launch_paged_plan(const PagedShape &s, const int *new_lens, const in
   cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (3 * kPagedMaxB + 2) * (int)sizeof(int));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   // one CTA while its threads take at most four rows each
   const int cl = s.T <= 4 * kPlThreads && s.B <= 4 * kPlThreads ? 1 : kPlCluster;

@@ -1,11 +1,20 @@
-// paged_tma.h -- tensor maps over a paged cache (bf16): tiles of `rows`
-// tokens by 64 elements (128 bytes), 128-byte swizzled, addressed as
-// (element, token of the page, page * Hkv + head).  Coordinates past the
-// pool, and tokens past a page's end, read zeros.
+// paged_tma.h -- tensor maps over a paged cache (bf16).  One copy brings the
+// part of a key tile that lies in one page, all d columns, in 128-byte rows of
+// 64 elements, 128-byte swizzled.  Two shared-memory layouts:
+//  * the whole tile is one part: [64-column block][key][128 B];
+//  * several parts: [8 keys][64-column block][key of the 8][128 B], so that the
+//    parts, one after another, make the same uniform layout.
+// (One copy per part and 64-column block, as a plain 2-D tile would need, is
+// bound by issuing the copies when pages are short: 16-token pages at d = 128
+// streamed at 5.2 TB/s, 32-token ones at 6.8.)  Coordinates past the pool, and
+// tokens past a single page's end, read zeros.
 #pragma once
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
 
 namespace sd {
 
@@ -18,11 +27,40 @@ inline int pg_part_rows(int page, int blocks, int KT) {
   return r;
 }
 
+// Byte strides of a tile's layout in shared memory: between groups of 8 keys,
+// between 64-column blocks.
+struct PgTile {
+  int part;  // keys of a part
+  int whole; // the tile is one part
+  int group, col;
+};
+inline PgTile pg_tile(int page, int blocks, int d, int KT) {
+  const int part = pg_part_rows(page, blocks, KT);
+  if (part == KT) return PgTile{part, 1, 1024, KT * 128};
+  return PgTile{part, 0, d / 64 * 1024, 1024};
+}
+
 cudaError_t pg_cache_map(CUtensorMap *map, const void *cache, int d, int page,
-                         long long pages_heads, int rows);
+                         long long pages_heads, const PgTile &t);
 // q [T, Hq, d] (tokens q_stride elements apart) as (element, head, token),
 // tiles of 64 elements x `heads` x `tokens`.
 cudaError_t pg_query_map(CUtensorMap *map, const void *q, int d, int Hq, int T,
                          long long q_stride, int heads, int tokens);
+
+#ifdef __CUDACC__
+// The part of a tile that starts at token y of page-and-head z.
+__device__ __forceinline__ void pg_tma_part(uint32_t dst, const CUtensorMap *map, const PgTile &t,
+                                            int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %2, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(t.whole ? y : 0), "r"(t.whole ? 0 : y >> 3), "r"(z),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void pg_prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+#endif
 
 }  // namespace sd

@@ -25,14 +25,15 @@ reads the device status (and synchronises); a capture needs check=False.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from . import (DTYPE_CODES, Workspace, _check, _need_cuda, _need_result, _ptr, _stream, load,
-               read_device_status)
+from . import DTYPE_CODES, Workspace, _check, _need_result, load, read_device_status
 
 _HEADER = 4096  # workspace bytes of the calls that only report a status
 _stream_ws: dict = {}
+_I32, _F32 = torch.int32, torch.float32
 
 
 class _PagedShape(ctypes.Structure):
@@ -41,58 +42,83 @@ class _PagedShape(ctypes.Structure):
                  "max_new")]
 
 
-def _shape(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new=0) -> _PagedShape:
+@functools.lru_cache(maxsize=512)
+def _shape(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new=0):
+    """The C shape of these sizes, by reference (read only by the library)."""
     if dtype not in DTYPE_CODES:
         raise TypeError(f"unsupported dtype {dtype}")
-    return _PagedShape(B, T, Hq, Hkv, d, DTYPE_CODES[dtype], page_size, num_pages, max_blocks,
-                       max_new)
+    return ctypes.byref(_PagedShape(B, T, Hq, Hkv, d, DTYPE_CODES[dtype], page_size, num_pages,
+                                    max_blocks, max_new))
 
 
-def _one_device(*ts) -> torch.device:
-    """The device all given tensors are on."""
+@functools.lru_cache(maxsize=512)
+def _attn_bytes(*sizes) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().sparse_paged_workspace_size(_shape(*sizes), ctypes.byref(n)), "paged_attn")
+    return int(n.value)
+
+
+def _one_device(*ts) -> int:
+    """The index of the device that all given tensors are on."""
     dev = None
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and on {t.device}")
-        dev = t.device
+        i = t.get_device()
+        if i != dev:
+            if i < 0:
+                raise ValueError("all tensors must be CUDA tensors")
+            if dev is not None:
+                raise ValueError(f"tensors on cuda:{dev} and on cuda:{i}")
+            dev = i
     return dev
 
 
-class _Scratch:
-    """The workspace buffer of one call: its pointer, and the status to read."""
+def _on(dev: int):
+    """Calls a function with device dev current."""
+    if torch.cuda.current_device() == dev:
+        return lambda f: f()
 
-    def __init__(self, ws: Workspace | None, device, nbytes: int, check: bool):
+    def guarded(f):
+        with torch.cuda.device(dev):
+            return f()
+    return guarded
+
+
+class _Scratch:
+    """The workspace buffer of one call on the current device: the C arguments
+    (buffer, bytes, stream), and the status to read."""
+
+    def __init__(self, ws: Workspace | None, dev: int, nbytes: int, check: bool):
+        stream = torch._C._cuda_getCurrentRawStream(dev)
         capturing = torch.cuda.is_current_stream_capturing()
         if capturing and check:
             raise ValueError("check=True synchronises: give check=False inside a stream capture")
-        self.ws = ws
         if ws is not None:
-            if ws.device.index not in (None, device.index):
-                raise ValueError(f"workspace on {ws.device}, tensors on {device}")
+            if ws.device.index not in (None, dev):
+                raise ValueError(f"workspace on {ws.device}, tensors on cuda:{dev}")
             if capturing and (ws.buf is None or ws.buf.numel() < nbytes):
                 raise ValueError("a workspace cannot grow inside a stream capture: "
                                  f"get({nbytes}) before it")
-            self.buf = ws.get(nbytes)
+            buf = ws.get(nbytes)
             if capturing:  # the graph keeps this address, also when ws grows later
-                ws.kept = getattr(ws, "kept", []) + [self.buf]
+                ws.kept = getattr(ws, "kept", []) + [buf]
         elif capturing:
-            # written before it is read, and never checked: no need to clear it
-            self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            # only the header has to start at zero: the graph clears it
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+            if nbytes > _HEADER:
+                buf[:_HEADER].zero_()
         else:
-            key = (device.index, torch.cuda.current_stream(device).cuda_stream)
-            if key not in _stream_ws:
-                _stream_ws[key] = Workspace(device)
-            self.ws = _stream_ws[key]
-            self.buf = self.ws.get(nbytes)
+            ws = _stream_ws.get((dev, stream))
+            if ws is None:
+                ws = _stream_ws[dev, stream] = Workspace(f"cuda:{dev}")
+            buf = ws.get(nbytes)
+        self.ws, self.buf = ws, buf
+        self.args = (buf.data_ptr(), buf.numel(), stream)
 
-    def args(self):
-        return _ptr(self.buf), self.buf.numel(), _stream()
-
-    def finish(self, check: bool):
+    def finish(self, rc: int, what: str, check: bool):
+        if rc:
+            _check(rc, what)
         if check:
             read_device_status(self.ws)
 
@@ -102,17 +128,19 @@ def _rows(t, name: str, heads: int, d: int) -> int:
     elements must be dense."""
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
         raise ValueError(f"{name} must be [T,{heads},{d}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != d):
         raise ValueError(f"the rows of {name} must be contiguous")
     if t.shape[0] < 2:
         return heads * d
-    if t.stride(0) < heads * d or t.stride(0) * t.element_size() % 16:
+    if st[0] < heads * d or st[0] * t.element_size() % 16:
         raise ValueError(f"the rows of {name} must be distinct and a multiple of 16 bytes apart")
-    return t.stride(0)
+    return st[0]
 
 
 def _need_int32(t, shape, name: str):
-    _need_result(t, shape, torch.int32, name)
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
+        _need_result(t, shape, _I32, name)
 
 
 def _cache_dims(K, V):
@@ -126,11 +154,7 @@ def _cache_dims(K, V):
 def paged_workspace_bytes(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks,
                           max_new: int | None = None) -> int:
     """Bytes that paged_attn needs of a workspace for these sizes."""
-    n = ctypes.c_size_t(0)
-    sh = _shape(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new or 0)
-    _check(load().sparse_paged_workspace_size(ctypes.byref(sh), ctypes.byref(n)),
-           "paged_workspace_size")
-    return int(n.value)
+    return _attn_bytes(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new or 0)
 
 
 def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: int,
@@ -152,32 +176,38 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
     if new_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("new_lens must be [B], block_table [B,max_blocks], free_pages [F]")
     B, T, F = new_lens.shape[0], int(num_tokens), free_pages.shape[0]
+    blocks = block_table.shape[1]
     if T < 0:
         raise ValueError("num_tokens must not be negative")
-    for t, s, name in [(new_lens, (B,), "new_lens"), (lens, (B,), "lens"),
-                       (block_table, (B, block_table.shape[1]), "block_table"),
-                       (free_pages, (F,), "free_pages"), (free_count, (1,), "free_count"),
-                       (kv_lens, (B,), "kv_lens"), (q_start, (B + 1,), "q_start"),
-                       (positions, (T,), "positions"), (slots, (T,), "slots"),
-                       (free_left, (1,), "free_left")]:
+    for t, s, name in ((new_lens, (B,), "new_lens"), (lens, (B,), "lens"),
+                       (block_table, (B, blocks), "block_table"),
+                       (free_pages, (F,), "free_pages"), (free_count, (1,), "free_count")):
         _need_int32(t, s, name)
-    sh = _shape(B, T, 1, 1, 64, torch.float32, int(page_size), int(num_pages),
-                block_table.shape[1])
-    with torch.cuda.device(dev):
+    sizes = (T, T, B, B + 1, 1)
+    res = [positions, slots, kv_lens, q_start, free_left]
+    names = ("positions", "slots", "kv_lens", "q_start", "free_left")
+    for i in range(5):
+        if res[i] is not None:
+            _need_int32(res[i], (sizes[i],), names[i])
+    sh = _shape(B, T, 1, 1, 64, _F32, int(page_size), int(num_pages), blocks)
+
+    def call():
         scratch = _Scratch(ws, dev, _HEADER, check)
-        new = {"dtype": torch.int32, "device": dev}
-        kv_lens = torch.empty(B, **new) if kv_lens is None else kv_lens
-        q_start = torch.empty(B + 1, **new) if q_start is None else q_start
-        positions = torch.empty(T, **new) if positions is None else positions
-        slots = torch.empty(T, **new) if slots is None else slots
-        free_left = torch.empty(1, **new) if free_left is None else free_left
-        _check(load().sparse_paged_plan(
-            ctypes.byref(sh), _ptr(new_lens), _ptr(lens), _ptr(block_table), _ptr(free_pages), F,
-            _ptr(free_count), _ptr(kv_lens), _ptr(q_start), _ptr(positions), _ptr(slots),
-            _ptr(free_left), *scratch.args()), "paged_plan")
-        scratch.finish(check)
-    return {"kv_lens": kv_lens, "q_start": q_start, "positions": positions, "slots": slots,
-            "free_left": free_left}
+        lack = [i for i in range(5) if res[i] is None]
+        if lack:  # one allocation for the results that were not given
+            want = [sizes[i] for i in lack]
+            for i, v in zip(lack, torch.empty(sum(want), dtype=_I32,
+                                              device=new_lens.device).split(want)):
+                res[i] = v
+        pos, slot, kv, start, left = res
+        scratch.finish(load().sparse_paged_plan(
+            sh, new_lens.data_ptr(), lens.data_ptr(), block_table.data_ptr(),
+            free_pages.data_ptr(), F, free_count.data_ptr(), kv.data_ptr(), start.data_ptr(),
+            pos.data_ptr(), slot.data_ptr(), left.data_ptr(), *scratch.args), "paged_plan", check)
+
+    _on(dev)(call)
+    return {"kv_lens": res[2], "q_start": res[3], "positions": res[0], "slots": res[1],
+            "free_left": res[4]}
 
 
 def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: bool = True):
@@ -197,12 +227,14 @@ def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: 
     sh = _shape(1, T, Hkv, Hkv, d, K.dtype, page, pages, 1)
     if T == 0:
         return
-    with torch.cuda.device(dev):
+
+    def call():
         scratch = _Scratch(ws, dev, _HEADER, check)
-        _check(load().sparse_paged_append(ctypes.byref(sh), _ptr(K), _ptr(V), _ptr(k_new), ks,
-                                          _ptr(v_new), vs, _ptr(slots), *scratch.args()),
-               "paged_append")
-        scratch.finish(check)
+        scratch.finish(load().sparse_paged_append(
+            sh, K.data_ptr(), V.data_ptr(), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+            slots.data_ptr(), *scratch.args), "paged_append", check)
+
+    _on(dev)(call)
 
 
 def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: int = 0,
@@ -223,7 +255,7 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
     pages, Hkv, page, d = _cache_dims(K, V)
     if q.dim() != 3 or q.dtype != K.dtype:
         raise ValueError("q must be [T,Hq,d] of the cache's dtype")
-    T, Hq = q.shape[:2]
+    T, Hq = q.shape[0], q.shape[1]
     qs = _rows(q, "q", Hq, d)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B,max_blocks]")
@@ -231,27 +263,30 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
     _need_int32(block_table, (B, blocks), "block_table")
     _need_int32(q_start, (B + 1,), "q_start")
     _need_int32(kv_lens, (B,), "kv_lens")
-    _need_result(out, (T, Hq, d), q.dtype, "out")
-    _need_result(lse, (T, Hq), torch.float32, "lse")
+    if out is not None:
+        _need_result(out, (T, Hq, d), q.dtype, "out")
+    if lse is not None:
+        _need_result(lse, (T, Hq), _F32, "lse")
     window, sinks = int(window), int(sinks)
     if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
         raise ValueError("window and sinks must not be negative")
     if max_new is not None and int(max_new) < 1:
         raise ValueError("max_new must be at least 1")
-    sh = _shape(B, T, Hq, Hkv, d, q.dtype, page, pages, blocks, int(max_new or 0))
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
-        if lse is None and return_lse:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        n = ctypes.c_size_t(0)
-        _check(load().sparse_paged_workspace_size(ctypes.byref(sh), ctypes.byref(n)),
-               "paged_attn")
-        if T == 0:
-            return out, lse
-        scratch = _Scratch(ws, dev, int(n.value), check)
-        _check(load().sparse_paged_attn(
-            ctypes.byref(sh), _ptr(q), qs, _ptr(K), _ptr(V), _ptr(block_table), _ptr(q_start),
-            _ptr(kv_lens), window, sinks, _ptr(out), _ptr(lse), *scratch.args()), "paged_attn")
-        scratch.finish(check)
+    sizes = (B, T, Hq, Hkv, d, K.dtype, page, pages, blocks, int(max_new or 0))
+    nbytes = _attn_bytes(*sizes)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
+    if T == 0:
+        return out, lse
+
+    def call():
+        scratch = _Scratch(ws, dev, nbytes, check)
+        scratch.finish(load().sparse_paged_attn(
+            _shape(*sizes), q.data_ptr(), qs, K.data_ptr(), V.data_ptr(), block_table.data_ptr(),
+            q_start.data_ptr(), kv_lens.data_ptr(), window, sinks, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), *scratch.args), "paged_attn", check)
+
+    _on(dev)(call)
     return out, lse
