@@ -40,7 +40,9 @@ sparse_status_t check_paged(const sparse_paged_shape_t *p, PagedShape *s) {
   if (s->page % 16 != 0 && s->blocks != 1) return SPARSE_ERR_UNSUPPORTED;
   if ((long long)s->pages * s->page > 0x7fffffffll ||
       (long long)s->pages * s->Hkv > 0x7fffffffll ||
-      (long long)s->blocks * s->page > (1ll << 30) || s->T > (1 << 24))
+      (long long)s->blocks * s->page > (1ll << 30) || s->T > (1 << 24) ||
+      // the 64-key tiles that the longest batch has, in 31 bits
+      (long long)s->B * s->Hkv * ((long long)s->blocks * s->page / 64 + 32) > 0x7fffffffll)
     return SPARSE_ERR_UNSUPPORTED;
   if (s->max_new == 0 || s->max_new > s->T) s->max_new = s->T;
   return SPARSE_OK;

@@ -9,16 +9,18 @@
 // partial (O, max, sum), and the last of the pair's runs to arrive merges them
 // in run order (so the result does not depend on which one that is).
 //
-// A CTA is two producer warps and four consumer warps.  The producers stream
+// A CTA is two producer warps and five or six consumer warps.  The producers stream
 // the run's K and V tiles through a ring of shared-memory stages with TMA (one
 // copy per page and tile, 128-byte swizzle), across pair boundaries, so the
-// ring never drains.  Each consumer warp takes every fourth tile with its own
-// running maximum, sum and O: S = Q K^T and O += P V on mma.sync m16n8k16 --
-// 16 rows are all there is, a quarter of the smallest tcgen05 tile, and nothing
-// has to leave the registers between the two products.  (Sharing each tile
-// between the warps, 16 keys each, made a tile's chain of latencies the limit
-// at d = 64.)  P is split in two bf16 parts (P_hi + P_lo: 16 significant bits),
-// which costs nothing where memory is the limit.
+// ring never drains.  Each consumer warp takes every fifth or sixth tile with its own
+// running maximum, sum and O (sharing a tile between the warps, 16 keys each,
+// made a tile's chain of latencies the limit at d = 64), on mma.sync m16n8k16
+// in the transposed form S^T = K Q^T, O^T += V^T P^T: the queries are the
+// instruction's 8 columns, so up to 8 rows cost half of what padding them to
+// the 16 (or 128) rows of the other operand would, and P^T only changes lanes
+// (an 8x8 transpose) between the two products.  P is split in two bf16 parts
+// (P_hi + P_lo: 16 significant bits), which costs little where memory is the
+// limit.
 #include "paged.h"
 #include "paged.cuh"
 #include "paged_tma.h"
@@ -27,35 +29,32 @@ namespace sd {
 namespace {
 
 constexpr int kDcKeys = 64;      // keys per tile
-constexpr int kDcWarps = 4;      // consumer warps
-constexpr int kDcThreads = 32 * (kDcWarps + 2);
-constexpr int kDcRows = 16;
 constexpr int kDcMerge = 8;      // partials merged at a time
 constexpr int kDcGroup = 16;     // runs of a pair merged at once
 static_assert(kPagedMaxRuns / kDcGroup <= kPagedTops, "a counter per stretch of kDcGroup runs");
 
-template <int D>
+// NT: groups of 8 query rows
+template <int D, int NT>
 struct DcCfg {
-  static constexpr int kTile = kDcKeys * D * 2;           // K or V of a tile
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kTile = kDcKeys * D * 2;  // K or V of a tile
+  static constexpr int kWarps = NT == 1 ? 6 : 5;  // consumer warps
+  static constexpr int kThreads = 32 * (kWarps + 2);
   // a multiple of the consumer warps: a stage's tiles all belong to one warp,
   // which has then seen every phase of the stage's barrier before the next (a
   // parity wait is only sound one phase ahead)
-  static constexpr int kStages = D == 128 ? 4 : 8;
-  static_assert(kStages % kDcWarps == 0, "a stage belongs to one warp");
+  static constexpr int kStages = (D == 128 ? 1 : 2) * kWarps;
   static constexpr int kRing = kStages * 2 * kTile;
-  static constexpr int kOS = D + 8;                        // floats between rows of O
-  static constexpr int kOBytes = kDcWarps * kDcRows * kOS * 4;
+  static constexpr int kOS = D + 4;              // floats between rows of O
+  static constexpr int kOBytes = kWarps * kRows * kOS * 4;
   static constexpr int kSmem = kRing + kOBytes + 1024 + 1024;  // + small, alignment
+  static_assert(kSmem <= 227 * 1024, "fits an SM");
 };
 
-// a / b, by 32-bit division where both allow it
-__device__ __forceinline__ long long div_ll(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
 // Where a run starts: sequence, KV head, tile of the pair.
 struct DcStart {
-  long long total, run;  // tiles of the call, tiles per run
-  int align;             // a pair's tiles are counted in multiples of this
+  int total, run;  // tiles of the call (the host bounds them below 2^31), tiles per run
+  int align;       // a pair's tiles are counted in multiples of this
   int b, h, u;
 };
 
@@ -84,62 +83,63 @@ constexpr int kDcAligns = 4;  // 1, 4, 8, 16: 1 or 2 << i
 // scan gives the total and the stretch's first tile, and the thread whose
 // stretch holds the run's first tile walks to it.  (A kernel of its own for
 // this cost a launch and 4 us of a one-request call.)
+template <int kThreads>
 __device__ __forceinline__ void dc_schedule(const PgArgs &a, DcStart *st,
-                                            long long (*sums)[kDcAligns]) {
+                                            int (*sums)[kDcAligns]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.B + kDcThreads - 1) / kDcThreads;
+  const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  long long mine[kDcAligns] = {}, x[kDcAligns];
+  int mine[kDcAligns] = {}, x[kDcAligns];
   for (int b = b0; b < b1; ++b) {
     const int u = dc_pair(a, b, blockIdx.x == 0);
 #pragma unroll
     for (int i = 0; i < kDcAligns; ++i)
-      mine[i] += (long long)a.Hkv * dc_round(u, i == 0 ? 1 : 2 << i);
+      mine[i] += a.Hkv * dc_round(u, i == 0 ? 1 : 2 << i);
   }
 #pragma unroll
   for (int i = 0; i < kDcAligns; ++i) {
     x[i] = mine[i];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long p = __shfl_up_sync(0xffffffffu, x[i], o);
+      const int p = __shfl_up_sync(0xffffffffu, x[i], o);
       if (lane >= o) x[i] += p;
     }
     if (lane == 31) sums[warp][i] = x[i];
   }
   __syncthreads();
   int pick = 0;
-  long long total = 0, run = 0, base = 0, part = 0;
+  int total = 0, run = 0, base = 0, part = 0;
 #pragma unroll
   for (int i = kDcAligns - 1; i >= 0; --i) {
-    long long t = 0, bs = x[i] - mine[i];
+    int t = 0, bs = x[i] - mine[i];
 #pragma unroll
-    for (int w = 0; w < kDcThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) bs += sums[w][i];
       t += sums[w][i];
     }
     const int al = 2 << i;
-    if (i == 0 || t <= (long long)gridDim.x * al) {
+    if (i == 0 || t <= (int)gridDim.x * al) {
       if (i > 0 || pick == 0) {
         pick = i;
         total = t;
         base = bs;
         part = mine[i];
-        run = i > 0 ? al : div_ll(t + gridDim.x - 1, gridDim.x);
+        run = i > 0 ? al : (int)((t + gridDim.x - 1) / gridDim.x);
       }
     }
   }
   const int align = pick > 0 ? 2 << pick : 1;
-  const long long x0 = (long long)blockIdx.x * run;
+  const long long x0 = (long long)blockIdx.x * run;  // may pass the total
   if (tid == 0) st->total = total, st->run = run, st->align = align;
   if (part > 0 && base <= x0 && x0 < base + part) {
     for (int b = b0; b < b1; ++b) {
       const int each = dc_round(dc_pair(a, b, false), align);
-      const long long t = (long long)a.Hkv * each;
+      const int t = a.Hkv * each;
       if (x0 < base + t) {
-        const long long off = x0 - base;
+        const int off = (int)x0 - base;
         st->b = b;
-        st->h = (int)div_ll(off, each);
-        st->u = (int)(off - (long long)st->h * each);
+        st->h = off / each;
+        st->u = off % each;
         break;
       }
       base += t;
@@ -158,7 +158,7 @@ struct DcSeg {
 
 // Walks a run's segments: every warp of the CTA takes the same walk.
 struct DcWalk {
-  long long left, item;  // tiles left in the run; the pair's first tile in the call's list
+  int left, item;  // tiles left in the run; the pair's first tile in the call's list
   int b, h, u, align;
   __device__ bool next(const PgArgs &a, DcSeg *s) {
     if (left <= 0) return false;
@@ -178,7 +178,7 @@ struct DcWalk {
     const int units = dc_units(s->t);
     s->units = dc_round(units, align);
     s->u0 = u;
-    const int end = (int)min((long long)s->units, u + left);
+    const int end = min(s->units, u + left);
     left -= end - u;
     s->cut = end - u < s->units;
     s->u1 = min(end, units);
@@ -218,15 +218,23 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
 }
-__device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kDcWarps) : "memory");
+// the transpose of an 8x8 block of 16-bit values held by the warp (lane: row
+// lane / 4, columns 2 (lane % 4), + 1)
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <int N>
+__device__ __forceinline__ void consumers_sync_n() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(kDcThreads, 1)
+template <int D, int NT>
+__global__ void __launch_bounds__(DcCfg<D, NT>::kThreads, 1)
     paged_decode_kernel(const PgArgs a, const __grid_constant__ CUtensorMap mapK,
                         const __grid_constant__ CUtensorMap mapV, const PgTile tl) {
-  using C = DcCfg<D>;
+  using C = DcCfg<D, NT>;
   extern __shared__ unsigned char raw[];
   const uint32_t raw_s = smem_u32(raw);
   const uint32_t base = (raw_s + 1023u) & ~1023u;
@@ -237,10 +245,10 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   uint64_t *empty = full + C::kStages;
   uint32_t *okmask = reinterpret_cast<uint32_t *>(empty + C::kStages);
   float *ml = reinterpret_cast<float *>(okmask + C::kStages);     // [warp][row][2]
-  uint32_t *flag = reinterpret_cast<uint32_t *>(ml + kDcWarps * kDcRows * 2);
+  uint32_t *flag = reinterpret_cast<uint32_t *>(ml + C::kWarps * C::kRows * 2);
   __shared__ DcStart s0;
-  __shared__ long long warp_sums[kDcThreads / 32][kDcAligns];
-  static_assert(C::kStages * 20 + kDcWarps * kDcRows * 8 + 4 <= 1024, "small area");
+  __shared__ int warp_sums[C::kThreads / 32][kDcAligns];
+  static_assert(C::kStages * 20 + C::kWarps * C::kRows * 8 + 4 <= 1024, "small area");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -255,17 +263,18 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
-  dc_schedule(a, &s0, warp_sums);
-  const long long run = s0.run, x0 = (long long)blockIdx.x * run;
-  if (x0 >= s0.total) return;
+  dc_schedule<C::kThreads>(a, &s0, warp_sums);
+  const int run = s0.run;
+  if ((long long)blockIdx.x * run >= s0.total) return;
+  const int x0 = blockIdx.x * run;
   DcWalk walk{min(run, s0.total - x0), x0 - s0.u, s0.b, s0.h, s0.u, s0.align};
   DcSeg seg;
   const int page = a.page, part_rows = tl.part;
   const int nparts = kDcKeys / part_rows, part_log = 31 - __clz(part_rows);
 
-  if (warp >= kDcWarps) {
+  if (warp >= C::kWarps) {
     // ---- producers: K, V ----------------------------------------------------------
-    const bool isV = warp > kDcWarps;
+    const bool isV = warp > C::kWarps;
     const CUtensorMap *map = isV ? &mapV : &mapK;
     const int per = 32 / nparts;  // tiles whose table entries the lanes hold
     int stage = 0, issued = 0;
@@ -334,24 +343,30 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   }
 
   // ---- consumers -----------------------------------------------------------------
+  auto consumers_sync = [] { consumers_sync_n<32 * C::kWarps>(); };
   const int G = a.Hq / a.Hkv;
   const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
   __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
   const int g8 = lane >> 2, t4 = lane & 3;
   // this warp's next tile of the run, and its stage
-  long long mine = warp, seg0 = 0;
+  int mine = warp, seg0 = 0;
   int stage = warp;
   uint32_t phase = 0;
   bool dead = false;  // a wait ran out: no further waiting, the results are void
   while (walk.next(a, &seg)) {
     const int rows = seg.n * G;
-    uint32_t qf[D / 16][4];
-    int pos[2], low[2];
+    // Q as the B operand: query 8 nt + g8, elements 16 s + 2 t4, + 8
+    uint32_t qf[NT][D / 16][2];
+    int pos[NT][2], low[NT][2];  // of queries 8 nt + 2 t4, + 1
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g8 + i * 8;
-      pos[i] = r < rows ? seg.p_first + r / G : -1;
-      low[i] = pg_window_low(pos[i], a.window);
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + t4 * 2 + e;
+        pos[nt][e] = r < rows ? seg.p_first + r / G : -1;
+        low[nt][e] = pg_window_low(pos[nt][e], a.window);
+      }
+      const int r = nt * 8 + g8;
       const uint32_t *src =
           r < rows ? reinterpret_cast<const uint32_t *>(
                          q + (size_t)(seg.row0 + r / G) * a.q_stride +
@@ -359,19 +374,25 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                    : nullptr;
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
-        qf[s][i] = src ? src[s * 8 + t4] : 0u;
-        qf[s][i + 2] = src ? src[s * 8 + t4 + 4] : 0u;
+        qf[nt][s][0] = src ? src[s * 8 + t4] : 0u;
+        qf[nt][s][1] = src ? src[s * 8 + t4 + 4] : 0u;
       }
     }
     // the last row's window is the tightest
     const int low_last = pg_window_low(seg.kv - 1, a.window);
-    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // O^T: row 16 dt + g8 (+ 8) of V's columns, queries 8 nt + 2 t4, + 1
+    float o[D / 16][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+    }
 
-    const long long seg1 = seg0 + seg.u1 - seg.u0;
-    for (; mine < seg1; mine += kDcWarps) {
-      const int key0 = seg.t.tile(seg.u0 + (int)(mine - seg0)) * kDcKeys;
+    const int seg1 = seg0 + seg.u1 - seg.u0;
+    for (; mine < seg1; mine += C::kWarps) {
+      const int key0 = seg.t.tile(seg.u0 + mine - seg0) * kDcKeys;
       if (!dead && !mbar_wait(&full[stage], phase, a.status)) dead = true;
       const uint32_t all_parts = (1u << nparts) - 1u, ok = okmask[stage] & all_parts;
       const uint32_t ks = base + stage * 2 * C::kTile, vs = ks + C::kTile;
@@ -396,21 +417,27 @@ __global__ void __launch_bounds__(kDcThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
       }
-      float sc[kDcKeys / 8][4];
+      // S^T = K Q^T: keys 16 mt + g8 (+ 8), queries 8 nt + 2 t4, + 1
+      constexpr int MT = kDcKeys / 16;
+      float sc[MT][NT][4];
 #pragma unroll
-      for (int i = 0; i < kDcKeys / 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          sc[i][nt][0] = sc[i][nt][1] = sc[i][nt][2] = sc[i][nt][3] = 0.f;
       {
-        const uint32_t row = ks + (lane >> 4) * tl.group + (lane & 7) * 128;
+        const uint32_t row = ks + ((lane >> 3) & 1) * tl.group + (lane & 7) * 128;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          const int ch = 2 * s + ((lane >> 3) & 1);
+          const int ch = 2 * s + (lane >> 4);
           const uint32_t at = row + (ch >> 3) * tl.col + (((ch & 7) ^ (lane & 7)) << 4);
 #pragma unroll
-          for (int kb = 0; kb < kDcKeys / 16; ++kb) {
+          for (int mt = 0; mt < MT; ++mt) {
             uint32_t kf[4];
-            ldsm4(at + kb * 2 * tl.group, kf);
-            mma16816(sc[2 * kb], qf[s], kf[0], kf[1]);
-            mma16816(sc[2 * kb + 1], qf[s], kf[2], kf[3]);
+            ldsm4(at + mt * 2 * tl.group, kf);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(sc[mt][nt], kf, qf[nt][s][0], qf[nt][s][1]);
           }
         }
       }
@@ -422,104 +449,116 @@ __global__ void __launch_bounds__(kDcThreads, 1)
           pages[w] = ((ok >> ((32 * w) >> part_log)) & 1u ? 0xffffu : 0u) |
                      ((ok >> ((32 * w + 16) >> part_log)) & 1u ? 0xffff0000u : 0u);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int hi = pos[i] - key0, lo = low[i] - key0, sk = a.sinks - key0;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            uint32_t see = pg_below(hi + 1 - 32 * w) &
-                           (~pg_below(lo - 32 * w) | pg_below(sk - 32 * w)) & pages[w];
-            see >>= t4 * 2;
+          for (int e = 0; e < 2; ++e) {
+            const int hi = pos[nt][e] - key0, lo = low[nt][e] - key0, sk = a.sinks - key0;
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+            for (int w = 0; w < 2; ++w) {
+              uint32_t see = pg_below(hi + 1 - 32 * w) &
+                             (~pg_below(lo - 32 * w) | pg_below(sk - 32 * w)) & pages[w];
+              see >>= g8;
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (!((see >> (nt * 8 + e)) & 1u)) sc[4 * w + nt][2 * i + e] = -INFINITY;
+              for (int i = 0; i < 4; ++i)
+                if (!((see >> (8 * i)) & 1u)) sc[2 * w + (i >> 1)][nt][(i & 1) * 2 + e] = -INFINITY;
+            }
+          }
+      }
+      float use[NT][2];
+      bool up = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) x = fmaxf(x, fmaxf(sc[mt][nt][e], sc[mt][nt][2 + e]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          mx[nt][e] = fmaxf(x * a.scale_log2, m[nt][e]);
+          use[nt][e] = mx[nt][e] == -INFINITY ? 0.f : mx[nt][e];
+          up |= mx[nt][e] > m[nt][e];
+        }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float c0 = exp2f(m[nt][0] - use[nt][0]), c1 = exp2f(m[nt][1] - use[nt][1]);
+          l[nt][0] *= c0;
+          l[nt][1] *= c1;
+          m[nt][0] = mx[nt][0];
+          m[nt][1] = mx[nt][1];
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[i][nt][0] *= c0;
+            o[i][nt][1] *= c1;
+            o[i][nt][2] *= c0;
+            o[i][nt][3] *= c1;
           }
         }
       }
-      float mx[2], use[2];
-      bool up = false;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[i] = -INFINITY;
+      for (int mt = 0; mt < MT; ++mt) {
+        // P^T of 16 keys as the B operand: 8x8 blocks transposed between lanes
+        uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < kDcKeys / 8; ++nt)
-          mx[i] = fmaxf(mx[i], fmaxf(sc[nt][2 * i], sc[nt][2 * i + 1]));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        mx[i] = fmaxf(mx[i] * a.scale_log2, m[i]);
-        use[i] = mx[i] == -INFINITY ? 0.f : mx[i];
-        up |= mx[i] > m[i];
-      }
-      if (__any_sync(0xffffffffu, up)) {
-        const float c0 = exp2f(m[0] - use[0]), c1 = exp2f(m[1] - use[1]);
-        l[0] *= c0;
-        l[1] *= c1;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= c0;
-          o[i][1] *= c0;
-          o[i][2] *= c1;
-          o[i][3] *= c1;
-        }
-        m[0] = mx[0];
-        m[1] = mx[1];
-      }
-#pragma unroll
-      for (int kb = 0; kb < kDcKeys / 16; ++kb) {
-        uint32_t ph[4], pl[4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float *x = &sc[2 * kb + nt][2 * i];
-            const float p0 = pg_exp2(fmaf(x[0], a.scale_log2, -use[i]));
-            const float p1 = pg_exp2(fmaf(x[1], a.scale_log2, -use[i]));
-            l[i] += p0 + p1;
+            const float p0 = pg_exp2(fmaf(sc[mt][nt][2 * i], a.scale_log2, -use[nt][0]));
+            const float p1 = pg_exp2(fmaf(sc[mt][nt][2 * i + 1], a.scale_log2, -use[nt][1]));
+            l[nt][0] += p0;
+            l[nt][1] += p1;
             const uint32_t hi = pack2(p0, p1);
-            ph[nt * 2 + i] = hi;
-            pl[nt * 2 + i] = pack2(p0 - __uint_as_float(hi << 16),
-                                   p1 - __uint_as_float(hi & 0xffff0000u));
+            ph[nt][i] = transpose8(hi);
+            pl[nt][i] = transpose8(pack2(p0 - __uint_as_float(hi << 16),
+                                         p1 - __uint_as_float(hi & 0xffff0000u)));
           }
-        const uint32_t row =
-            vs + (2 * kb + ((lane >> 3) & 1)) * tl.group + (lane & 7) * 128;
+        // O^T += V^T P^T
+        const uint32_t row = vs + (2 * mt + (lane >> 4)) * tl.group + (lane & 7) * 128;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const int ch = 2 * s + (lane >> 4);
+        for (int dt = 0; dt < D / 16; ++dt) {
+          const int ch = 2 * dt + ((lane >> 3) & 1);
           uint32_t vf[4];
           ldsm4t(row + (ch >> 3) * tl.col + (((ch & 7) ^ (lane & 7)) << 4), vf);
-          mma16816(o[2 * s], ph, vf[0], vf[1]);
-          mma16816(o[2 * s + 1], ph, vf[2], vf[3]);
-          mma16816(o[2 * s], pl, vf[0], vf[1]);
-          mma16816(o[2 * s + 1], pl, vf[2], vf[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(o[dt][nt], vf, ph[nt][0], ph[nt][1]);
+            mma16816(o[dt][nt], vf, pl[nt][0], pl[nt][1]);
+          }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stage]);
-      stage += kDcWarps;
+      stage += C::kWarps;
       if (stage >= C::kStages) stage -= C::kStages, phase ^= 1u;
     }
     seg0 = seg1;
 
-    // ---- the four warps' parts of the segment, joined in shared memory ---------
+    // ---- the warps' parts of the segment, joined in shared memory ---------
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      const int r = g8 + i * 8;
-      if (t4 == 0) {
-        ml[(warp * kDcRows + r) * 2] = m[i];
-        ml[(warp * kDcRows + r) * 2 + 1] = l[i];
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[nt][e];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int r = warp * C::kRows + nt * 8 + t4 * 2 + e;
+        if (g8 == 0) {
+          ml[r * 2] = m[nt][e];
+          ml[r * 2 + 1] = sum;
+        }
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) {
+          os[r * C::kOS + dt * 16 + g8] = o[dt][nt][e];
+          os[r * C::kOS + dt * 16 + g8 + 8] = o[dt][nt][2 + e];
+        }
       }
-      float *dst = os + (warp * kDcRows + r) * C::kOS + t4 * 2;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c)
-        *reinterpret_cast<float2 *>(dst + c * 8) = make_float2(o[c][2 * i], o[c][2 * i + 1]);
-    }
     consumers_sync();
     // the pair's first and last run
-    const int first = (int)div_ll(walk.item, run);
-    const int last_run = (int)div_ll(walk.item + seg.units - 1, run);
+    const int first = walk.item / run, last_run = (walk.item + seg.units - 1) / run;
     const size_t per = (size_t)a.part_rows * D;
     float2 *pml = reinterpret_cast<float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
     const size_t slot = 2 * (size_t)blockIdx.x + (seg.u0 == 0 ? 1 : 0);
@@ -533,20 +572,20 @@ __global__ void __launch_bounds__(kDcThreads, 1)
       if (a.lse && c == 0)
         a.lse[at] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
     };
-    for (int i = tid; i < rows * (D / 4); i += 32 * kDcWarps) {
+    for (int i = tid; i < rows * (D / 4); i += 32 * C::kWarps) {
       const int r = i / (D / 4), c = i % (D / 4);
       float mm = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kDcWarps; ++w) mm = fmaxf(mm, ml[(w * kDcRows + r) * 2]);
+      for (int w = 0; w < C::kWarps; ++w) mm = fmaxf(mm, ml[(w * C::kRows + r) * 2]);
       const float us = mm == -INFINITY ? 0.f : mm;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float ll = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDcWarps; ++w) {
-        const float f = exp2f(ml[(w * kDcRows + r) * 2] - us);
-        ll += ml[(w * kDcRows + r) * 2 + 1] * f;
+      for (int w = 0; w < C::kWarps; ++w) {
+        const float f = exp2f(ml[(w * C::kRows + r) * 2] - us);
+        ll += ml[(w * C::kRows + r) * 2 + 1] * f;
         const float4 v =
-            *reinterpret_cast<const float4 *>(os + (w * kDcRows + r) * C::kOS + c * 4);
+            *reinterpret_cast<const float4 *>(os + (w * C::kRows + r) * C::kOS + c * 4);
         acc.x += v.x * f;
         acc.y += v.y * f;
         acc.z += v.z * f;
@@ -576,7 +615,7 @@ __global__ void __launch_bounds__(kDcThreads, 1)
       // merges the partials of runs w0, w0 + step, .. (n of them); the result
       // is the pair's output, or replaces the first one
       auto merge = [&](int w0, int step, int n, bool final) {
-        for (int i = tid; i < kDcRows * (D / 4); i += 32 * kDcWarps) {
+        for (int i = tid; i < C::kRows * (D / 4); i += 32 * C::kWarps) {
           const int r = i / (D / 4), c = i % (D / 4);
           if (r >= rows) break;
           float mm = -INFINITY, ll = 0.f;
@@ -650,13 +689,13 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   }
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
-  using C = DcCfg<D>;
+  using C = DcCfg<D, NT>;
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
-  auto kern = paged_decode_kernel<D>;
+  auto kern = paged_decode_kernel<D, NT>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const PgTile tile = pg_tile(s.page, s.blocks, D, kDcKeys);
@@ -670,7 +709,7 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = attrs;
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(kDcThreads, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.numAttrs = 0;
   add_pdl_attr(cfg, attrs);
@@ -678,10 +717,15 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+template <int D>
+cudaError_t pick(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
+  return s.max_new * s.G() <= 8 ? run<D, 1>(s, a, st) : run<D, 2>(s, a, st);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_decode(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
-  return s.d == 64 ? run<64>(s, a, st) : run<128>(s, a, st);
+  return s.d == 64 ? pick<64>(s, a, st) : pick<128>(s, a, st);
 }
 
 }  // namespace sd
