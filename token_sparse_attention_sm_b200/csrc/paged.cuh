@@ -30,12 +30,30 @@ struct PgHead {
   uint32_t pad[15];
 };
 
+// Division of n in [0, 2^31) by a divisor the host knows: the multiplier is
+// floor(2^(31+s) / d) + 1 with 2^(s-1) < d <= 2^s, whose error stays below one
+// part in 2^31 of the quotient's unit.
+struct PgDiv {
+  uint32_t mul;
+  int shift;  // s - 1; -1: d = 1
+  __device__ __forceinline__ int operator()(int n) const {
+    return shift < 0 ? n : (int)(__umulhi((uint32_t)n, mul) >> shift);
+  }
+};
+inline PgDiv pg_divisor(uint32_t d) {
+  int s = 0;
+  while ((1u << s) < d) ++s;
+  return s == 0 ? PgDiv{0, -1} : PgDiv{(uint32_t)(((1ull << (31 + s)) / d) + 1), s - 1};
+}
+
 struct PgArgs {
   const void *q, *K, *V;
   const int *table, *q_start, *kv_lens;
   void *out;
   float *lse;
   long long q_stride;  // elements between the tokens of q
+  int G;            // Hq / Hkv
+  PgDiv by_G, by_page;
   int B, T, Hq, Hkv, page, pages, blocks, window, sinks, max_new;
   float scale_log2;
   uint32_t *status;

@@ -172,6 +172,9 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
   a.T = s.T;
   a.Hq = s.Hq;
   a.Hkv = s.Hkv;
+  a.G = s.G();
+  a.by_G = sd::pg_divisor((uint32_t)a.G);
+  a.by_page = sd::pg_divisor((uint32_t)s.page);
   a.page = s.page;
   a.pages = s.pages;
   a.blocks = s.blocks;

@@ -54,9 +54,9 @@ __device__ __forceinline__ void load_tile(float *dst, unsigned char *kok, const 
     bool ok = j < limit && (j >= low || j < a.sinks);
     size_t off = 0;
     if (ok) {
-      const int pg = table[j / a.page];
+      const int blk = a.by_page(j), pg = table[blk];
       ok = pg >= 0 && pg < a.pages;
-      if (ok) off = (((size_t)pg * a.Hkv + h) * a.page + j % a.page) * D + c * PER;
+      if (ok) off = (((size_t)pg * a.Hkv + h) * a.page + j - blk * a.page) * D + c * PER;
       else if (c == 0) raise_flag(a.status, FLAG_INDEX);
     }
     if (kok && c == 0) kok[r] = ok;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
   int *box = reinterpret_cast<int *>(Ps + RB * PS);
   unsigned char *kok = reinterpret_cast<unsigned char *>(box + 16);
   const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
-  const int G = a.Hq / a.Hkv, TB = RB / G;
+  const int G = a.G, TB = RB / G;
   const float *q = static_cast<const float *>(a.q), *K = static_cast<const float *>(a.K),
               *V = static_cast<const float *>(a.V);
   float *out = static_cast<float *>(a.out);
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
       const int r = p / (D / 4), c = p % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
-        const float *src = q + (size_t)(row0 + t0 + r / G) * a.q_stride + (h * G + r % G) * D + c * 4;
+        const float *src = q + (size_t)(row0 + t0 + a.by_G(r)) * a.q_stride + (h * G + r - a.by_G(r) * G) * D + c * 4;
         v = *reinterpret_cast<const float4 *>(src);
       }
       *reinterpret_cast<float4 *>(Qs + r * QS + c * 4) = v;
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
-      pos[i] = r < rows ? p_first + r / G : -1;
+      pos[i] = r < rows ? p_first + a.by_G(r) : -1;
       lowr[i] = pg_window_low(pos[i], a.window);
     }
     if (u0 < u1)
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
       for (int i = 0; i < 4; ++i) {
         const int r = ty * 4 + i;
         if (r >= rows) continue;
-        const size_t tok = (size_t)(row0 + t0 + r / G), hq = h * G + r % G;
+        const size_t tok = (size_t)(row0 + t0 + a.by_G(r)), hq = h * G + r - a.by_G(r) * G;
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
               acc[c] += __ldcg(&a.part[s * per + (size_t)r * D + c * 32 + lane]) * w;
           }
           const float inv = ll > 0.f ? 1.f / ll : 0.f;
-          const size_t tok = (size_t)(row0 + t0 + r / G), hq = h * G + r % G;
+          const size_t tok = (size_t)(row0 + t0 + a.by_G(r)), hq = h * G + r - a.by_G(r) * G;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
             out[(tok * a.Hq + hq) * D + c * 32 + lane] = acc[c] * inv;

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   const uint32_t base = (raw_s + 1023u) & ~1023u;
   ChSmall *sm = reinterpret_cast<ChSmall *>(raw + (base - raw_s) + C::kSmallOff);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int G = a.Hq / a.Hkv, TPT = 128 / G, TB = 2 * TPT;  // tokens per row tile, per block
+  const int G = a.G, TPT = 128 / G, TB = 2 * TPT;  // tokens per row tile, per block
 
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             const int j0 = (u < sink_tiles ? u : u - sink_tiles + lo) * kChKeys +
                            (lane % nparts) * tl.part;
             if (j0 < limit && (j0 + tl.part > low || j0 < a.sinks)) {
-              const int blk = (int)((uint32_t)j0 / (uint32_t)a.page), e = table[blk];
+              const int blk = a.by_page(j0), e = table[blk];
               if (e >= 0 && e < a.pages) {
                 yy = j0 - blk * a.page;
                 zz = e * a.Hkv + h;
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       }
       const int br = t * tile_rows + r;  // row of the block
       const bool live = r < tile_rows && br < I.rows;
-      const int pos = live ? I.p_first + br / G : -1;
+      const int pos = live ? I.p_first + a.by_G(br) : -1;
       const int low = pg_window_low(pos, a.window);
       const int pf = I.p_first + t * TPT, pl = min(I.p_last, pf + TPT - 1);  // the tile's tokens
       const int low_last = pg_window_low(pl, a.window);
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) break;
         ch_fence_after();
       }
-      const size_t at = (size_t)(I.row0 + I.t0 + br / G) * a.Hq + I.h * G + br % G;
+      const size_t at = (size_t)(I.row0 + I.t0 + a.by_G(br)) * a.Hq + I.h * G + br - a.by_G(br) * G;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const size_t per = (size_t)a.part_rows * D;
       const size_t first = (size_t)I.first * a.Hkv + I.h;
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             }
           }
           const float iv = ll > 0.f ? 1.f / ll : 0.f;
-          const size_t o = (size_t)(I.row0 + I.t0 + row / G) * a.Hq + I.h * G + row % G;
+          const size_t o = (size_t)(I.row0 + I.t0 + a.by_G(row)) * a.Hq + I.h * G + row - a.by_G(row) * G;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
             out[o * D + c * 32 + lane] = __float2bfloat16_rn(acc[c] * iv);

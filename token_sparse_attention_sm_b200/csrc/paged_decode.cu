@@ -9,10 +9,10 @@
 // partial (O, max, sum), and the last of the pair's runs to arrive merges them
 // in run order (so the result does not depend on which one that is).
 //
-// A CTA is two producer warps and five or six consumer warps.  The producers stream
+// A CTA is two or four producer warps and four or six consumer warps.  The producers stream
 // the run's K and V tiles through a ring of shared-memory stages with TMA (one
 // copy per page and tile, 128-byte swizzle), across pair boundaries, so the
-// ring never drains.  Each consumer warp takes every fifth or sixth tile with its own
+// ring never drains.  Each consumer warp takes every fourth or sixth tile with its own
 // running maximum, sum and O (sharing a tile between the warps, 16 keys each,
 // made a tile's chain of latencies the limit at d = 64), on mma.sync m16n8k16
 // in the transposed form S^T = K Q^T, O^T += V^T P^T: the queries are the
@@ -38,12 +38,17 @@ template <int D, int NT>
 struct DcCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kTile = kDcKeys * D * 2;  // K or V of a tile
-  static constexpr int kWarps = NT == 1 ? 6 : 5;  // consumer warps
-  static constexpr int kThreads = 32 * (kWarps + 2);
+  static constexpr int kWarps = NT == 1 ? 6 : 4;  // consumer warps
+  // pairs of producer warps: d = 64 tiles are half as long and as many copies
+  // (16-token pages at d = 64: 34.2 -> 30.2 us for 64 windows of 4,095 tokens;
+  // at d = 128 the registers of two more warps cost more than they bring)
+  static constexpr int kPairs = D == 64 || NT == 2 ? 2 : 1;
+  static constexpr int kThreads = 32 * (kWarps + 2 * kPairs);
   // a multiple of the consumer warps: a stage's tiles all belong to one warp,
   // which has then seen every phase of the stage's barrier before the next (a
   // parity wait is only sound one phase ahead)
   static constexpr int kStages = (D == 128 ? 1 : 2) * kWarps;
+  static_assert(kStages % kPairs == 0, "and to one pair of producers");
   static constexpr int kRing = kStages * 2 * kTile;
   static constexpr int kOS = D + 4;              // floats between rows of O
   static constexpr int kOBytes = kWarps * kRows * kOS * 4;
@@ -232,7 +237,7 @@ __device__ __forceinline__ void consumers_sync_n() {
 
 template <int D, int NT>
 __global__ void __launch_bounds__(DcCfg<D, NT>::kThreads, 1)
-    paged_decode_kernel(const PgArgs a, const __grid_constant__ CUtensorMap mapK,
+    paged_decode_kernel(const __grid_constant__ PgArgs a, const __grid_constant__ CUtensorMap mapK,
                         const __grid_constant__ CUtensorMap mapV, const PgTile tl) {
   using C = DcCfg<D, NT>;
   extern __shared__ unsigned char raw[];
@@ -260,6 +265,10 @@ __global__ void __launch_bounds__(DcCfg<D, NT>::kThreads, 1)
     pg_prefetch_map(&mapK);
     pg_prefetch_map(&mapV);
   }
+  // the arguments through the constant cache once, while the kernel before may
+  // still run: a first touch later would stall the one chain there is
+  __shared__ volatile uint32_t touched[sizeof(PgArgs) / 4];
+  if (tid < (int)(sizeof(PgArgs) / 4)) touched[tid] = reinterpret_cast<const uint32_t *>(&a)[tid];
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
@@ -273,11 +282,12 @@ __global__ void __launch_bounds__(DcCfg<D, NT>::kThreads, 1)
   const int nparts = kDcKeys / part_rows, part_log = 31 - __clz(part_rows);
 
   if (warp >= C::kWarps) {
-    // ---- producers: K, V ----------------------------------------------------------
-    const bool isV = warp > C::kWarps;
+    // ---- producers: K and V, of every tile or of the even and the odd ones ---------
+    const bool isV = (warp - C::kWarps) & 1;
+    const int odd = (warp - C::kWarps) >> 1;
     const CUtensorMap *map = isV ? &mapV : &mapK;
     const int per = 32 / nparts;  // tiles whose table entries the lanes hold
-    int stage = 0, issued = 0;
+    int stage = odd, at = 0, last = -1;  // at: tiles of the run before the one considered
     uint32_t phase = 0;
     bool alive = true;
     while (alive && walk.next(a, &seg)) {
@@ -294,7 +304,7 @@ __global__ void __launch_bounds__(DcCfg<D, NT>::kThreads, 1)
           const int j0 = seg.t.tile(u) * kDcKeys + (lane % nparts) * part_rows;
           // some row sees one of the part's keys
           if (j0 < seg.limit && (j0 + part_rows > seg.low || j0 < a.sinks)) {
-            const int blk = (int)((uint32_t)j0 / (uint32_t)page), e = table[blk];
+            const int blk = a.by_page(j0), e = table[blk];
             if (e >= 0 && e < a.pages) {
               yy = j0 - blk * page;
               zz = e * a.Hkv + seg.h;
@@ -313,7 +323,8 @@ __global__ void __launch_bounds__(DcCfg<D, NT>::kThreads, 1)
         const int cy = y, cz = z;
         const uint32_t cbad = __ballot_sync(0xffffffffu, bad);
         fetch(ub + per);
-        for (int u = ub; u < min(seg.u1, ub + per); ++u) {
+        for (int u = ub; u < min(seg.u1, ub + per); ++u, ++at) {
+          if (at % C::kPairs != odd) continue;
           const int src = (u - ub) * nparts + lane % nparts;
           const int ty = __shfl_sync(0xffffffffu, cy, src);
           const int tz = __shfl_sync(0xffffffffu, cz, src);
@@ -330,21 +341,22 @@ __global__ void __launch_bounds__(DcCfg<D, NT>::kThreads, 1)
             pg_tma_part(base + (2 * stage + isV) * C::kTile + lane * part_rows * (D * 2), map, tl,
                         ty, tz, &full[stage]);
           __syncwarp();
-          if (++stage == C::kStages) stage = 0, phase ^= 1u;
-          ++issued;
+          last = at;
+          stage += C::kPairs;
+          if (stage >= C::kStages) stage -= C::kStages, phase ^= 1u;
         }
       }
       walk.advance(a, seg);
     }
     // this warp's copies have landed before it leaves, whatever happened
-    for (int i = max(0, issued - C::kStages); i < issued; ++i)
+    for (int i = last; i >= max(0, last - C::kStages + 1); i -= C::kPairs)
       mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, a.status);
     return;
   }
 
   // ---- consumers -----------------------------------------------------------------
   auto consumers_sync = [] { consumers_sync_n<32 * C::kWarps>(); };
-  const int G = a.Hq / a.Hkv;
+  const int G = a.G;
   const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
   __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
   const int g8 = lane >> 2, t4 = lane & 3;
@@ -363,14 +375,14 @@ __global__ void __launch_bounds__(DcCfg<D, NT>::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = nt * 8 + t4 * 2 + e;
-        pos[nt][e] = r < rows ? seg.p_first + r / G : -1;
+        pos[nt][e] = r < rows ? seg.p_first + a.by_G(r) : -1;
         low[nt][e] = pg_window_low(pos[nt][e], a.window);
       }
       const int r = nt * 8 + g8;
       const uint32_t *src =
           r < rows ? reinterpret_cast<const uint32_t *>(
-                         q + (size_t)(seg.row0 + r / G) * a.q_stride +
-                         (size_t)(seg.h * G + r % G) * D)
+                         q + (size_t)(seg.row0 + a.by_G(r)) * a.q_stride +
+                         (size_t)(seg.h * G + r - a.by_G(r) * G) * D)
                    : nullptr;
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
@@ -378,6 +390,8 @@ __global__ void __launch_bounds__(DcCfg<D, NT>::kThreads, 1)
         qf[nt][s][1] = src ? src[s * 8 + t4 + 4] : 0u;
       }
     }
+    // the pair's first and last run (divided here, where the tile is waited for)
+    const int first = walk.item / run, last_run = (walk.item + seg.units - 1) / run;
     // the last row's window is the tightest
     const int low_last = pg_window_low(seg.kv - 1, a.window);
     // O^T: row 16 dt + g8 (+ 8) of V's columns, queries 8 nt + 2 t4, + 1
@@ -557,14 +571,12 @@ __global__ void __launch_bounds__(DcCfg<D, NT>::kThreads, 1)
         }
       }
     consumers_sync();
-    // the pair's first and last run
-    const int first = walk.item / run, last_run = (walk.item + seg.units - 1) / run;
     const size_t per = (size_t)a.part_rows * D;
     float2 *pml = reinterpret_cast<float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
     const size_t slot = 2 * (size_t)blockIdx.x + (seg.u0 == 0 ? 1 : 0);
     auto store = [&](int r, int c, float4 acc, float mm, float ll) {
       const float inv = ll > 0.f ? 1.f / ll : 0.f;
-      const size_t at = (size_t)(seg.row0 + r / G) * a.Hq + seg.h * G + r % G;
+      const size_t at = (size_t)(seg.row0 + a.by_G(r)) * a.Hq + seg.h * G + r - a.by_G(r) * G;
       uint2 pk;
       pk.x = pack2(acc.x * inv, acc.y * inv);
       pk.y = pack2(acc.z * inv, acc.w * inv);
