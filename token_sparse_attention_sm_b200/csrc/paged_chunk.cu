@@ -11,7 +11,7 @@
 // Roles (384 threads, one warp idle):
 //  * two TMA warps, one of which claims the items and copies Q, stream K and V
 //    tiles through one ring (one copy per page and tile, 128-byte swizzle);
-//  * one thread issues the MMAs: S_t = Q_t K^T (M = N = 128) and O_t += P_t V,
+//  * one warp issues the MMAs: S_t = Q_t K^T (M = N = 128) and O_t += P_t V,
 //    P_t read from tensor memory;
 //  * four softmax warps per row tile, one row per thread: S from tensor
 //    memory, the row's maximum, P = exp2(S scale - m) rounded to bf16 over the
@@ -145,6 +145,18 @@ __device__ __forceinline__ void ch_tma(uint32_t dst, const CUtensorMap *map, int
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+// one lane of a converged warp, always the same
+__device__ __forceinline__ bool ch_elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+// a value that is the same in all lanes of a converged warp
+template <typename T>
+__device__ __forceinline__ T ch_uniform(T x) {
+  return __shfl_sync(0xffffffffu, x, 0);
 }
 __device__ __forceinline__ uint32_t ch_pack(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -366,94 +378,116 @@ __global__ void __launch_bounds__(kChThreads, 1)
       for (int at = 2 * unit - 2 + isV; at >= max(0, 2 * unit - C::kSlots); at -= 2)
         mbar_wait(&sm->full[at % C::kSlots], (at / C::kSlots) & 1, a.status);
     } else if (warp == kChMmaWarp) {
-      // ---- MMA thread ------------------------------------------------------------------
-      if (lane == 0) {
-        constexpr uint32_t idS = ch_idesc(kChKeys, false), idPV = ch_idesc(D, true);
-        int slot = 0;                 // ring position of the next K tile
-        uint32_t phase = 0;
-        int q_count = 0;              // items with tiles so far
-        uint32_t p_cnt[2] = {0, 0}, pv_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};
-        bool ok = true;
-        auto step = [&]() {
-          if (++slot == C::kSlots) slot = 0, phase ^= 1u;
-        };
-        auto issue_s = [&](int t, int kslot) {
-          const uint64_t q = ch_desc(base + C::kQOff + t * C::kQTile, 16, 1024);
-          const uint64_t k = ch_desc(base + C::kRingOff + kslot * C::kTile, 16, tl.group);
-          const uint32_t kcol = tl.col / 16;
-  #pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            // the address field of a descriptor counts 16-byte units
-            ch_mma_ss(tmem + t * 128, q + ((s >> 2) * (128 * 128) + (s & 3) * 32) / 16,
+      // ---- MMA warp: all lanes walk, one issues ----------------------------------------
+      // (The walk stays uniform and the issue under elect.sync, so the operands
+      // live in uniform registers: issued from a divergent lane 0, with each
+      // descriptor moved over on its own, an instruction took about 100 cycles.)
+      constexpr uint32_t idS = ch_idesc(kChKeys, false), idPV = ch_idesc(D, true);
+      const bool lead = ch_elect();
+      const uint32_t tm = ch_uniform(tmem), base_u = ch_uniform(base);
+      int slot = 0;  // ring position of the next K tile
+      uint32_t phase = 0;
+      uint32_t q_count = 0;  // items with tiles so far
+      uint32_t p_cnt[2] = {0, 0}, pv_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};
+      auto step = [&]() {
+        if (++slot == C::kSlots) slot = 0, phase ^= 1u;
+      };
+      auto issue_s = [&](int t, int kslot) {
+        // the address field of a descriptor counts 16-byte units
+        const uint64_t q = ch_desc(base_u + C::kQOff + t * C::kQTile, 16, 1024);
+        const uint64_t k =
+            ch_desc(ch_uniform(base_u + C::kRingOff + kslot * C::kTile), 16, tl.group);
+        const uint32_t kcol = tl.col / 16;
+        if (lead) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            ch_mma_ss(tm + t * 128, q + ((s >> 2) * (128 * 128) + (s & 3) * 32) / 16,
                       k + (s >> 2) * kcol + (s & 3) * 2, idS, s > 0);
-          }
           ch_commit(&sm->s_full[t]);
-        };
-        for (int it = 0;; ++it) {
-          if (!ch_wait(&sm->item_full[it & 1], (it >> 1) & 1, sm, a.status)) break;
-          const ChItem &I = sm->item[it & 1];
-          const int valid = I.valid, n = I.u1 - I.u0, tiles = I.rows > TPT * G ? 2 : 1;
-          mbar_arrive(&sm->item_empty[it & 1]);
-          if (!valid) break;
-          if (n <= 0) continue;
-          if (!(ok = ch_wait(&sm->q_full, q_count & 1, sm, a.status))) break;
-          ++q_count;
-          // S of the first key tile
-          if (!(ok = ch_wait(&sm->full[slot], phase, sm, a.status))) break;
-          for (int t = 0; t < tiles && ok; ++t) {
-            // the last P of the item before is used up
-            if (pv_cnt[t] > 0) ok = ch_wait(&sm->pv_done[t], (pv_cnt[t] - 1) & 1, sm, a.status);
+        }
+        __syncwarp();
+      };
+      auto issue_pv = [&](int t, int vslot, uint32_t accumulate) {
+        const uint64_t v =
+            ch_desc(ch_uniform(base_u + C::kRingOff + vslot * C::kTile), tl.col, tl.group);
+        const uint32_t vstep = 2 * tl.group / 16;  // 16 keys
+        if (lead) {
+#pragma unroll
+          for (int kk = 0; kk < kChKeys / 16; ++kk)
+            ch_mma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8, v + kk * vstep, idPV,
+                      kk > 0 ? 1u : accumulate);
+          ch_commit(&sm->pv_done[t]);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t *bar) {
+        if (lead) ch_commit(bar);
+        __syncwarp();
+      };
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, ch_wait(bar, parity & 1u, sm, a.status)) != 0;
+      };
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        if (!(ok = wait(&sm->item_full[it & 1], it >> 1))) break;
+        const ChItem &I = sm->item[it & 1];
+        const int valid = ch_uniform(I.valid), n = ch_uniform(I.u1 - I.u0);
+        const bool two = ch_uniform(I.rows) > TPT * G;  // row tiles
+        __syncwarp();
+        if (lead) mbar_arrive(&sm->item_empty[it & 1]);
+        if (!valid) break;
+        if (n <= 0) continue;
+        // S of the first key tile
+        if (!(ok = wait(&sm->q_full, q_count++) && wait(&sm->full[slot], phase))) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t == 1 && !two) break;
+          // the last P of the item before is used up
+          if (ok && pv_cnt[t] > 0) ok = wait(&sm->pv_done[t], pv_cnt[t] - 1);
+          if (!ok) break;
+          ch_fence_after();
+          issue_s(t, slot);
+        }
+        if (!ok) break;
+        commit(&sm->empty[slot]);
+        if (n == 1) commit(&sm->q_empty);
+        step();
+        for (int j = 0; j < n && ok; ++j) {
+          const int vslot = slot;
+          const uint32_t vphase = phase;
+          step();  // slot: the next K
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t == 1 && !two) break;
+            if (!ok) break;
+            ok = wait(&sm->p_ready[t], p_cnt[t]++);
+            if (ok && t == 0) ok = wait(&sm->full[vslot], vphase);
+            if (j == 0) {  // O of the item before has been read
+              if (ok && o_cnt[t] > 0) ok = wait(&sm->o_empty[t], o_cnt[t] - 1);
+              ++o_cnt[t];
+            }
             if (!ok) break;
             ch_fence_after();
-            issue_s(t, slot);
-          }
-          if (!ok) break;
-          ch_commit(&sm->empty[slot]);
-          if (n == 1) ch_commit(&sm->q_empty);
-          step();
-          for (int j = 0; j < n && ok; ++j) {
-            const int vslot = slot;
-            const uint32_t vphase = phase;
-            step();  // slot: the next K
-            for (int t = 0; t < tiles && ok; ++t) {
-              ok = ch_wait(&sm->p_ready[t], p_cnt[t] & 1, sm, a.status);
-              ++p_cnt[t];
-              if (ok && t == 0) ok = ch_wait(&sm->full[vslot], vphase, sm, a.status);
-              // O of the item before has been read
-              if (ok && j == 0 && o_cnt[t] > 0)
-                ok = ch_wait(&sm->o_empty[t], (o_cnt[t] - 1) & 1, sm, a.status);
-              if (j == 0) ++o_cnt[t];
+            issue_pv(t, vslot, j > 0);
+            ++pv_cnt[t];
+            const bool last = t == 1 || !two;
+            if (last) commit(&sm->empty[vslot]);
+            if (j + 1 < n) {
+              if (t == 0) ok = wait(&sm->full[slot], phase);
+              // S_t overwrites the P_t that the product just issued reads
+              if (ok) ok = wait(&sm->pv_done[t], pv_cnt[t] - 1);
               if (!ok) break;
               ch_fence_after();
-              const uint64_t v =
-                  ch_desc(base + C::kRingOff + vslot * C::kTile, tl.col, tl.group);
-              const uint32_t vstep = 2 * tl.group / 16;  // 16 keys
-  #pragma unroll
-              for (int kk = 0; kk < kChKeys / 16; ++kk)
-                ch_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
-                          v + kk * vstep, idPV, j > 0 || kk > 0);
-              ch_commit(&sm->pv_done[t]);
-              ++pv_cnt[t];
-              if (t == tiles - 1) ch_commit(&sm->empty[vslot]);
-              if (j + 1 < n) {
-                if (t == 0) ok = ch_wait(&sm->full[slot], phase, sm, a.status);
-                // S_t overwrites the P_t that the product just issued reads
-                if (ok) ok = ch_wait(&sm->pv_done[t], (pv_cnt[t] - 1) & 1, sm, a.status);
-                if (!ok) break;
-                ch_fence_after();
-                issue_s(t, slot);
-                if (t == tiles - 1) {
-                  ch_commit(&sm->empty[slot]);
-                  if (j + 2 == n) ch_commit(&sm->q_empty);
-                }
+              issue_s(t, slot);
+              if (last) {
+                commit(&sm->empty[slot]);
+                if (j + 2 == n) commit(&sm->q_empty);
               }
             }
-            if (j + 1 < n) step();
           }
-          if (!ok) break;
+          if (j + 1 < n) step();
         }
       }
-      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChSoftRegs));
