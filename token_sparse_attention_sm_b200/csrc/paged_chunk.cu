@@ -8,16 +8,21 @@
 // Both row tiles use every K and V tile, which halves what one reads from L2
 // (at 128 rows the tile loads alone would ask for more than L2 gives).
 //
-// Roles (384 threads, one warp idle):
+// Roles (384 threads):
 //  * two TMA warps, one of which claims the items and copies Q, stream K and V
 //    tiles through one ring (one copy per page and tile, 128-byte swizzle);
-//  * one warp issues the MMAs: S_t = Q_t K^T (M = N = 128) and O_t += P_t V,
-//    P_t read from tensor memory;
+//  * a warp per row tile issues its MMAs: S_t = Q_t K^T (M = N = 128) and
+//    O_t += P_t V, P_t read from tensor memory;
 //  * four softmax warps per row tile, one row per thread: S from tensor
 //    memory, the row's maximum, P = exp2(S scale - m) rounded to bf16 over the
-//    dead S, and O scaled when the maximum moves.
-// The two row tiles alternate: while one's softmax runs, the other's products
-// do.  Tensor memory: S_0, S_1, O_0, O_1 (512 columns at d = 128).
+//    dead S, in two halves so that the product starts on the first, and O
+//    scaled when the maximum moves.
+// A row tile is one chain, scores - softmax - product - scores; the two tiles'
+// chains run side by side, and each has its own issuing warp so that neither
+// waits behind the other's waits.  Tensor memory: S_0, S_1, O_0, O_1 (512
+// columns at d = 128).  (Two 64-key S buffers per row tile took the turn-round
+// out of the chain but cost more: M = 128, N = 64 reads as much of Q for half
+// the work, 725 against 904 TFLOP/s on a 2,048-token chunk of 32K.)
 //
 // The reference m of a row is only raised when the running maximum has left it
 // by more than 2^8: weights then reach 256 instead of 1, the sums stay fp32,
@@ -37,11 +42,11 @@ namespace {
 
 constexpr int kChKeys = 128;
 constexpr int kChSoftWarps = 8;
-constexpr int kChThreads = 384;  // three warpgroups: two of softmax warps; MMA, K and V copies, one idle
+constexpr int kChThreads = 384;  // three warpgroups: two of softmax warps; MMA and copies
 // registers a thread: 168 at launch, moved from the third warpgroup to the
-// softmax ones (2 * 128 * 200 + 128 * 104 = 384 * 168)
-constexpr int kChSoftRegs = 200, kChOtherRegs = 104;
-constexpr int kChMmaWarp = kChSoftWarps, kChTmaWarp = kChSoftWarps + 1;  // K's, then V's
+// softmax ones (2 * 128 * 224 + 128 * 56 = 384 * 168)
+constexpr int kChSoftRegs = 224, kChOtherRegs = 56;
+constexpr int kChMmaWarp = kChSoftWarps, kChTmaWarp = kChSoftWarps + 2;  // row tiles' MMA; K, V
 constexpr float kChLag = 8.f;  // log2 units the maximum may run ahead of its reference
 
 template <int D>
@@ -68,7 +73,7 @@ struct ChItem {
 struct ChSmall {
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_ready[2], pv_done[2], o_empty[2], wg[2];
+  uint64_t s_full[2], p_ready[2][2], pv_done[2], o_empty[2], wg[2];  // p_ready: half a tile each
   uint64_t item_full[2], item_empty[2];
   ChItem item[2];
   uint32_t ok[8];
@@ -146,6 +151,31 @@ __device__ __forceinline__ void ch_tma(uint32_t dst, const CUtensorMap *map, int
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
+// pairs of fp32 values in one 64-bit register, and packed arithmetic on them
+__device__ __forceinline__ uint64_t ch_u2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t ch_f2(float lo, float hi) {
+  return ch_u2(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ void ch_split(uint64_t x, float *lo, float *hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(x));
+  *lo = __uint_as_float(a);
+  *hi = __uint_as_float(b);
+}
+__device__ __forceinline__ uint64_t ch_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t ch_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // one lane of a converged warp, always the same
 __device__ __forceinline__ bool ch_elect() {
   uint32_t p;
@@ -204,18 +234,19 @@ __global__ void __launch_bounds__(kChThreads, 1)
     sm->abort = 0;
     for (int i = 0; i < 8; ++i) {
       mbar_init(&sm->full[i], 1);
-      mbar_init(&sm->empty[i], 1);
+      mbar_init(&sm->empty[i], 2);  // both row tiles
     }
     mbar_init(&sm->q_full, 1);
-    mbar_init(&sm->q_empty, 1);
+    mbar_init(&sm->q_empty, 2);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm->s_full[t], 1);
-      mbar_init(&sm->p_ready[t], 4);
+      mbar_init(&sm->p_ready[t][0], 4);
+      mbar_init(&sm->p_ready[t][1], 4);
       mbar_init(&sm->pv_done[t], 1);
       mbar_init(&sm->o_empty[t], 4);
       mbar_init(&sm->wg[t], 4);
       mbar_init(&sm->item_full[t], 1);
-      mbar_init(&sm->item_empty[t], kChSoftWarps + 2);
+      mbar_init(&sm->item_empty[t], kChSoftWarps + 3);
     }
     fence_mbar_init();
     pg_prefetch_map(&mapQ);
@@ -377,115 +408,96 @@ __global__ void __launch_bounds__(kChThreads, 1)
       // last kSlots positions of the ring: an older slot has moved on)
       for (int at = 2 * unit - 2 + isV; at >= max(0, 2 * unit - C::kSlots); at -= 2)
         mbar_wait(&sm->full[at % C::kSlots], (at / C::kSlots) & 1, a.status);
-    } else if (warp == kChMmaWarp) {
-      // ---- MMA warp: all lanes walk, one issues ----------------------------------------
+    } else {
+      // ---- MMA warps, one per row tile: all lanes walk, one issues ---------------------
       // (The walk stays uniform and the issue under elect.sync, so the operands
       // live in uniform registers: issued from a divergent lane 0, with each
       // descriptor moved over on its own, an instruction took about 100 cycles.)
+      const int t = warp - kChMmaWarp;
       constexpr uint32_t idS = ch_idesc(kChKeys, false), idPV = ch_idesc(D, true);
       const bool lead = ch_elect();
-      const uint32_t tm = ch_uniform(tmem), base_u = ch_uniform(base);
-      int slot = 0;  // ring position of the next K tile
-      uint32_t phase = 0;
-      uint32_t q_count = 0;  // items with tiles so far
-      uint32_t p_cnt[2] = {0, 0}, pv_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};
+      const uint32_t tS = ch_uniform(tmem + t * 128), tO = ch_uniform(tmem + 256 + t * 128);
+      const uint64_t q = ch_desc(ch_uniform(base + C::kQOff + t * C::kQTile), 16, 1024);
+      const uint32_t ring = ch_uniform(base + C::kRingOff);
+      const uint32_t kcol = tl.col / 16, vstep = 2 * tl.group / 16;  // 16-byte units
+      int slot = 0;  // ring position of the next tile
+      uint32_t phase = 0, q_count = 0, pv_cnt = 0, o_cnt = 0;
       auto step = [&]() {
         if (++slot == C::kSlots) slot = 0, phase ^= 1u;
       };
-      auto issue_s = [&](int t, int kslot) {
-        // the address field of a descriptor counts 16-byte units
-        const uint64_t q = ch_desc(base_u + C::kQOff + t * C::kQTile, 16, 1024);
-        const uint64_t k =
-            ch_desc(ch_uniform(base_u + C::kRingOff + kslot * C::kTile), 16, tl.group);
-        const uint32_t kcol = tl.col / 16;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, ch_wait(bar, parity & 1u, sm, a.status)) != 0;
+      };
+      // S of the K tile in the ring's next slot, which it frees
+      auto scores = [&](bool last) {
+        const uint64_t k = ch_desc(ch_uniform(ring + slot * C::kTile), 16, tl.group);
         if (lead) {
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
-            ch_mma_ss(tm + t * 128, q + ((s >> 2) * (128 * 128) + (s & 3) * 32) / 16,
+            ch_mma_ss(tS, q + ((s >> 2) * (128 * 128) + (s & 3) * 32) / 16,
                       k + (s >> 2) * kcol + (s & 3) * 2, idS, s > 0);
           ch_commit(&sm->s_full[t]);
+          ch_commit(&sm->empty[slot]);
+          if (last) ch_commit(&sm->q_empty);
         }
         __syncwarp();
-      };
-      auto issue_pv = [&](int t, int vslot, uint32_t accumulate) {
-        const uint64_t v =
-            ch_desc(ch_uniform(base_u + C::kRingOff + vslot * C::kTile), tl.col, tl.group);
-        const uint32_t vstep = 2 * tl.group / 16;  // 16 keys
-        if (lead) {
-#pragma unroll
-          for (int kk = 0; kk < kChKeys / 16; ++kk)
-            ch_mma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8, v + kk * vstep, idPV,
-                      kk > 0 ? 1u : accumulate);
-          ch_commit(&sm->pv_done[t]);
-        }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t *bar) {
-        if (lead) ch_commit(bar);
-        __syncwarp();
-      };
-      auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, ch_wait(bar, parity & 1u, sm, a.status)) != 0;
+        step();
       };
       bool ok = true;
       for (int it = 0; ok; ++it) {
         if (!(ok = wait(&sm->item_full[it & 1], it >> 1))) break;
         const ChItem &I = sm->item[it & 1];
         const int valid = ch_uniform(I.valid), n = ch_uniform(I.u1 - I.u0);
-        const bool two = ch_uniform(I.rows) > TPT * G;  // row tiles
+        const bool mine = t == 0 || ch_uniform(I.rows) > TPT * G;
         __syncwarp();
         if (lead) mbar_arrive(&sm->item_empty[it & 1]);
         if (!valid) break;
         if (n <= 0) continue;
-        // S of the first key tile
-        if (!(ok = wait(&sm->q_full, q_count++) && wait(&sm->full[slot], phase))) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t == 1 && !two) break;
-          // the last P of the item before is used up
-          if (ok && pv_cnt[t] > 0) ok = wait(&sm->pv_done[t], pv_cnt[t] - 1);
-          if (!ok) break;
-          ch_fence_after();
-          issue_s(t, slot);
-        }
-        if (!ok) break;
-        commit(&sm->empty[slot]);
-        if (n == 1) commit(&sm->q_empty);
-        step();
-        for (int j = 0; j < n && ok; ++j) {
-          const int vslot = slot;
-          const uint32_t vphase = phase;
-          step();  // slot: the next K
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t == 1 && !two) break;
-            if (!ok) break;
-            ok = wait(&sm->p_ready[t], p_cnt[t]++);
-            if (ok && t == 0) ok = wait(&sm->full[vslot], vphase);
-            if (j == 0) {  // O of the item before has been read
-              if (ok && o_cnt[t] > 0) ok = wait(&sm->o_empty[t], o_cnt[t] - 1);
-              ++o_cnt[t];
-            }
-            if (!ok) break;
-            ch_fence_after();
-            issue_pv(t, vslot, j > 0);
-            ++pv_cnt[t];
-            const bool last = t == 1 || !two;
-            if (last) commit(&sm->empty[vslot]);
-            if (j + 1 < n) {
-              if (t == 0) ok = wait(&sm->full[slot], phase);
-              // S_t overwrites the P_t that the product just issued reads
-              if (ok) ok = wait(&sm->pv_done[t], pv_cnt[t] - 1);
-              if (!ok) break;
-              ch_fence_after();
-              issue_s(t, slot);
-              if (last) {
-                commit(&sm->empty[slot]);
-                if (j + 2 == n) commit(&sm->q_empty);
-              }
-            }
+        if (!(ok = wait(&sm->q_full, q_count++))) break;
+        if (!mine) {  // no rows in this tile: free what the other one uses
+          for (int j = 0; j < 2 * n && ok; ++j) {
+            ok = wait(&sm->full[slot], phase);
+            if (lead) mbar_arrive(&sm->empty[slot]);
+            step();
           }
-          if (j + 1 < n) step();
+          if (lead) mbar_arrive(&sm->q_empty);
+          __syncwarp();
+          continue;
+        }
+        // (the last P of the item before was used up: its end was waited for)
+        if (!(ok = wait(&sm->full[slot], phase))) break;
+        ch_fence_after();
+        scores(n == 1);
+        for (int j = 0; j < n && ok; ++j) {
+          if (!(ok = wait(&sm->full[slot], phase))) break;
+          if (j == 0 && o_cnt++ > 0)  // O of the item before has been read
+            if (!(ok = wait(&sm->o_empty[t], o_cnt - 2))) break;
+          const uint64_t v = ch_desc(ch_uniform(ring + slot * C::kTile), tl.col, tl.group);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!(ok = wait(&sm->p_ready[t][h], pv_cnt))) break;
+            ch_fence_after();
+            if (lead) {
+#pragma unroll
+              for (int kk = h * 4; kk < h * 4 + 4; ++kk)
+                ch_mma_ts(tO, tS + kk * 8, v + kk * vstep, idPV, kk > 0 ? 1u : (uint32_t)(j > 0));
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (lead) {
+            ch_commit(&sm->pv_done[t]);
+            ch_commit(&sm->empty[slot]);
+          }
+          __syncwarp();
+          step();
+          if (j + 1 < n && !(ok = wait(&sm->full[slot], phase))) break;
+          // S overwrites the P that the product just issued reads
+          if (!(ok = wait(&sm->pv_done[t], pv_cnt++))) break;
+          if (j + 1 < n) {
+            ch_fence_after();
+            scores(j + 2 == n);
+          }
         }
       }
     }
@@ -553,8 +565,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
         ch_fence_after();
         const uint32_t good = sm->ok[unit & 7];
         ++unit;
-        if (t == 0 && (key0 + kChKeys > I.p_last + 1 || (key0 < I.low && key0 + kChKeys > a.sinks))) {
+        if (key0 + kChKeys > I.p_last + 1 || (key0 < I.low && key0 + kChKeys > a.sinks)) {
           // V rows that no row of the block sees may hold anything: clear them
+          // (each tile's warps before its own product; both write zeros)
           const int key = key0 + r;
           if (key > I.p_last || (key < I.low && key >= a.sinks)) {
             const uint32_t v =
@@ -570,29 +583,54 @@ __global__ void __launch_bounds__(kChThreads, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        uint32_t s[128];
+        const bool whole = key0 + kChKeys - 1 <= pf &&
+                           (key0 >= low_last || key0 + kChKeys <= a.sinks) && good == all_ok;
+        uint32_t s[128], p[32];
+        uint64_t sum2[2];
+        const uint64_t scale2 = ch_f2(a.scale_log2, a.scale_log2);
+        // weights of keys 64 c .. 64 c + 63 against the reference m
+        auto weights = [&](int c, bool fresh) {
+          const float use = m == -INFINITY ? 0.f : m;
+          const uint64_t neg2 = ch_f2(-use, -use);
+          if (fresh) sum2[0] = sum2[1] = 0ull;  // pairs of zeros
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ch_ld32(tS + c * 32, s + c * 32);
+          for (int i = 0; i < 32; ++i) {
+            const int k = c * 64 + i * 2;
+            float p0, p1;
+            ch_split(ch_fma2(ch_u2(s[k], s[k + 1]), scale2, neg2), &p0, &p1);
+            p0 = pg_exp2(p0);
+            p1 = pg_exp2(p1);
+            sum2[i & 1] = ch_add2(sum2[i & 1], ch_f2(p0, p1));
+            p[i] = ch_pack(p0, p1);
+          }
+        };
+        // four accumulators, each block's maximum while the next one is read
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        ch_ld32(tS, s);
         ch_wait_ld();
-        if (key0 + kChKeys - 1 > pf || (key0 < low_last && key0 + kChKeys > a.sinks) ||
-            good != all_ok) {
-          // the row's keys of the tile, a bit each
-          const int hi = pos - key0, lo = low - key0, sk = a.sinks - key0;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t pages = ((good >> (2 * w)) & 1u ? 0xffffu : 0u) |
-                                   ((good >> (2 * w)) & 2u ? 0xffff0000u : 0u);
-            const uint32_t see = pg_below(hi + 1 - 32 * w) &
-                                 (~pg_below(lo - 32 * w) | pg_below(sk - 32 * w)) & pages;
+        for (int c = 0; c < 4; ++c) {
+          if (c < 3) ch_ld32(tS + (c + 1) * 32, s + (c + 1) * 32);
+          if (!whole) {
+            // the row's keys of the block, a bit each
+            const int hi = pos - key0, lo = low - key0, sk = a.sinks - key0;
+            const uint32_t pages = ((good >> (2 * c)) & 1u ? 0xffffu : 0u) |
+                                   ((good >> (2 * c)) & 2u ? 0xffff0000u : 0u);
+            const uint32_t see = pg_below(hi + 1 - 32 * c) &
+                                 (~pg_below(lo - 32 * c) | pg_below(sk - 32 * c)) & pages;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (!((see >> i) & 1u)) s[w * 32 + i] = 0xff800000u;
+              if (!((see >> i) & 1u)) s[c * 32 + i] = 0xff800000u;
           }
-        }
-        float mx = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
-        mx *= a.scale_log2;
+          for (int i = 0; i < 32; ++i)
+            mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(s[c * 32 + i]));
+          if (c < 3) ch_wait_ld();
+        }
+        // the first half's weights do not wait for the maximum: the reference
+        // rarely moves, and if it does they are taken again
+        weights(0, true);
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
         const bool raise = mx > m + kChLag || (m == -INFINITY && mx > m);
         if (__any_sync(0xffffffffu, raise)) {
           const float mn = raise ? mx : m;
@@ -603,35 +641,27 @@ __global__ void __launch_bounds__(kChThreads, 1)
             // the product before has finished: S of this tile came after it
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              ch_ld32(tO + c * 32, o);
+              ch_ld32(tO + c * 32, p);
               ch_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-              ch_st32(tO + c * 32, o);
+              for (int i = 0; i < 32; ++i) p[i] = __float_as_uint(__uint_as_float(p[i]) * corr);
+              ch_st32(tO + c * 32, p);
             }
           }
+          weights(0, true);
         }
-        const float use = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t p[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int k = c * 64 + i * 2;
-            const float p0 = pg_exp2(fmaf(__uint_as_float(s[k]), a.scale_log2, -use));
-            const float p1 = pg_exp2(fmaf(__uint_as_float(s[k + 1]), a.scale_log2, -use));
-            sum[i & 3] += p0 + p1;
-            p[i] = ch_pack(p0, p1);
-          }
+          if (c == 1) weights(1, false);
           ch_st32(tS + c * 32, p);
+          ch_wait_st();
+          ch_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->p_ready[t][c]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        ch_wait_st();
-        ch_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->p_ready[t]);
+        float a0, a1;
+        ch_split(ch_add2(sum2[0], sum2[1]), &a0, &a1);
+        l += a0 + a1;
       }
       if (!ok) break;
       // ---- the piece's result ----------------------------------------------------------
