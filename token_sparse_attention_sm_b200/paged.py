@@ -52,10 +52,12 @@ def _shape(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new=0)
 
 
 @functools.lru_cache(maxsize=512)
-def _attn_bytes(*sizes) -> int:
+def _attn_plan(*sizes):
+    """The C shape of an attention call and the workspace bytes it needs."""
     n = ctypes.c_size_t(0)
-    _check(load().sparse_paged_workspace_size(_shape(*sizes), ctypes.byref(n)), "paged_attn")
-    return int(n.value)
+    sh = _shape(*sizes)
+    _check(load().sparse_paged_workspace_size(sh, ctypes.byref(n)), "paged_attn")
+    return sh, int(n.value)
 
 
 def _one_device(*ts) -> int:
@@ -74,53 +76,38 @@ def _one_device(*ts) -> int:
     return dev
 
 
-def _on(dev: int):
-    """Calls a function with device dev current."""
-    if torch.cuda.current_device() == dev:
-        return lambda f: f()
-
-    def guarded(f):
-        with torch.cuda.device(dev):
-            return f()
-    return guarded
-
-
-class _Scratch:
-    """The workspace buffer of one call on the current device: the C arguments
-    (buffer, bytes, stream), and the status to read."""
-
-    def __init__(self, ws: Workspace | None, dev: int, nbytes: int, check: bool):
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-        capturing = torch.cuda.is_current_stream_capturing()
-        if capturing and check:
+def _scratch(ws: Workspace | None, dev: int, nbytes: int, check: bool):
+    """The workspace of one call on the current device: the buffer, and the
+    current stream."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.is_current_stream_capturing():
+        if check:
             raise ValueError("check=True synchronises: give check=False inside a stream capture")
-        if ws is not None:
-            if ws.device.index not in (None, dev):
-                raise ValueError(f"workspace on {ws.device}, tensors on cuda:{dev}")
-            if capturing and (ws.buf is None or ws.buf.numel() < nbytes):
-                raise ValueError("a workspace cannot grow inside a stream capture: "
-                                 f"get({nbytes}) before it")
-            buf = ws.get(nbytes)
-            if capturing:  # the graph keeps this address, also when ws grows later
-                ws.kept = getattr(ws, "kept", []) + [buf]
-        elif capturing:
+        if ws is None:
             # only the header has to start at zero: the graph clears it
             buf = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
             if nbytes > _HEADER:
                 buf[:_HEADER].zero_()
-        else:
-            ws = _stream_ws.get((dev, stream))
-            if ws is None:
-                ws = _stream_ws[dev, stream] = Workspace(f"cuda:{dev}")
-            buf = ws.get(nbytes)
-        self.ws, self.buf = ws, buf
-        self.args = (buf.data_ptr(), buf.numel(), stream)
+            return None, buf, stream
+        if ws.buf is None or ws.buf.numel() < nbytes:
+            raise ValueError("a workspace cannot grow inside a stream capture: "
+                             f"get({nbytes}) before it")
+        # the graph keeps this address, also when ws grows later
+        ws.kept = getattr(ws, "kept", []) + [ws.buf]
+    elif ws is None:
+        ws = _stream_ws.get((dev, stream))
+        if ws is None:
+            ws = _stream_ws[dev, stream] = Workspace(f"cuda:{dev}")
+    if ws.device.index not in (None, dev):
+        raise ValueError(f"workspace on {ws.device}, tensors on cuda:{dev}")
+    return ws, ws.get(nbytes), stream
 
-    def finish(self, rc: int, what: str, check: bool):
-        if rc:
-            _check(rc, what)
-        if check:
-            read_device_status(self.ws)
+
+def _finish(rc: int, what: str, ws, check: bool):
+    if rc:
+        _check(rc, what)
+    if check:
+        read_device_status(ws)
 
 
 def _rows(t, name: str, heads: int, d: int) -> int:
@@ -154,7 +141,7 @@ def _cache_dims(K, V):
 def paged_workspace_bytes(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks,
                           max_new: int | None = None) -> int:
     """Bytes that paged_attn needs of a workspace for these sizes."""
-    return _attn_bytes(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new or 0)
+    return _attn_plan(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new or 0)[1]
 
 
 def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: int,
@@ -190,24 +177,26 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
         if res[i] is not None:
             _need_int32(res[i], (sizes[i],), names[i])
     sh = _shape(B, T, 1, 1, 64, _F32, int(page_size), int(num_pages), blocks)
-
-    def call():
-        scratch = _Scratch(ws, dev, _HEADER, check)
-        lack = [i for i in range(5) if res[i] is None]
-        if lack:  # one allocation for the results that were not given
-            want = [sizes[i] for i in lack]
-            for i, v in zip(lack, torch.empty(sum(want), dtype=_I32,
-                                              device=new_lens.device).split(want)):
-                res[i] = v
-        pos, slot, kv, start, left = res
-        scratch.finish(load().sparse_paged_plan(
-            sh, new_lens.data_ptr(), lens.data_ptr(), block_table.data_ptr(),
-            free_pages.data_ptr(), F, free_count.data_ptr(), kv.data_ptr(), start.data_ptr(),
-            pos.data_ptr(), slot.data_ptr(), left.data_ptr(), *scratch.args), "paged_plan", check)
-
-    _on(dev)(call)
-    return {"kv_lens": res[2], "q_start": res[3], "positions": res[0], "slots": res[1],
-            "free_left": res[4]}
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size,
+                              num_tokens, num_pages, ws, check, kv_lens, q_start, positions, slots,
+                              free_left)
+    w, buf, stream = _scratch(ws, dev, _HEADER, check)
+    lack = [i for i in range(5) if res[i] is None]
+    if lack:  # one allocation for the results that were not given
+        want = [sizes[i] for i in lack]
+        new = torch.empty(sum(want), dtype=_I32, device=new_lens.device).split(want)
+        for i, v in zip(lack, new):
+            res[i] = v
+    positions, slots, kv_lens, q_start, free_left = res
+    _finish(load().sparse_paged_plan(
+        sh, new_lens.data_ptr(), lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), F,
+        free_count.data_ptr(), kv_lens.data_ptr(), q_start.data_ptr(), positions.data_ptr(),
+        slots.data_ptr(), free_left.data_ptr(), buf.data_ptr(), buf.numel(), stream),
+        "paged_plan", w, check)
+    return {"kv_lens": kv_lens, "q_start": q_start, "positions": positions, "slots": slots,
+            "free_left": free_left}
 
 
 def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: bool = True):
@@ -227,14 +216,13 @@ def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: 
     sh = _shape(1, T, Hkv, Hkv, d, K.dtype, page, pages, 1)
     if T == 0:
         return
-
-    def call():
-        scratch = _Scratch(ws, dev, _HEADER, check)
-        scratch.finish(load().sparse_paged_append(
-            sh, K.data_ptr(), V.data_ptr(), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
-            slots.data_ptr(), *scratch.args), "paged_append", check)
-
-    _on(dev)(call)
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return paged_append(K, V, k_new, v_new, slots, ws, check)
+    w, buf, stream = _scratch(ws, dev, _HEADER, check)
+    _finish(load().sparse_paged_append(
+        sh, K.data_ptr(), V.data_ptr(), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+        slots.data_ptr(), buf.data_ptr(), buf.numel(), stream), "paged_append", w, check)
 
 
 def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: int = 0,
@@ -272,21 +260,21 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
         raise ValueError("window and sinks must not be negative")
     if max_new is not None and int(max_new) < 1:
         raise ValueError("max_new must be at least 1")
-    sizes = (B, T, Hq, Hkv, d, K.dtype, page, pages, blocks, int(max_new or 0))
-    nbytes = _attn_bytes(*sizes)
+    sh, nbytes = _attn_plan(B, T, Hq, Hkv, d, K.dtype, page, pages, blocks, int(max_new or 0))
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return paged_attn(q, K, V, block_table, q_start, kv_lens, window, sinks, max_new, ws,
+                              check, return_lse, out, lse)
     if out is None:
         out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
     if T == 0:
         return out, lse
-
-    def call():
-        scratch = _Scratch(ws, dev, nbytes, check)
-        scratch.finish(load().sparse_paged_attn(
-            _shape(*sizes), q.data_ptr(), qs, K.data_ptr(), V.data_ptr(), block_table.data_ptr(),
-            q_start.data_ptr(), kv_lens.data_ptr(), window, sinks, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), *scratch.args), "paged_attn", check)
-
-    _on(dev)(call)
+    w, buf, stream = _scratch(ws, dev, nbytes, check)
+    _finish(load().sparse_paged_attn(
+        sh, q.data_ptr(), qs, K.data_ptr(), V.data_ptr(), block_table.data_ptr(),
+        q_start.data_ptr(), kv_lens.data_ptr(), window, sinks, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), stream),
+        "paged_attn", w, check)
     return out, lse
