@@ -12,6 +12,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace sd {
@@ -136,6 +138,82 @@ __device__ __forceinline__ int pg_find(const PgSeq *seqs, int B, int x, PgSeq *o
   }
   *out = seqs[lo];
   return lo;
+}
+
+// Merges the np partials of `rows` rows from row0 on, in piece order, by nt
+// threads; out and lse get the result.  slot0 is the first piece's partial,
+// the others follow a.Hkv apart; at(row) is a row's place in out [T, Hq].
+// Several elements and pieces are loaded together: row by row, one piece after
+// another, this was a tail of 80 us (13 pieces of 64 rows).
+template <int D, typename T, typename At>
+__device__ __forceinline__ void pg_merge(const PgArgs &a, size_t slot0, int np, int row0, int rows,
+                                         int tid, int nt, At at, T *out) {
+  constexpr int E = 4, P = 4;  // elements of a thread, pieces at a time
+  const size_t per = (size_t)a.part_rows * D;
+  const float2 *ml = reinterpret_cast<const float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
+  const int total = rows * (D / 4);
+  for (int i0 = tid; i0 < total; i0 += E * nt) {
+    float m[E], l[E];
+    float4 acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      m[e] = -INFINITY;
+      l[e] = 0.f;
+      acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int p0 = 0; p0 < np; p0 += P) {
+      float2 x[E][P];
+      float4 v[E][P];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int i = min(i0 + e * nt, total - 1), row = row0 + i / (D / 4), c = i % (D / 4);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const size_t s = slot0 + (size_t)min(p0 + p, np - 1) * a.Hkv;
+          x[e][p] = __ldcg(&ml[s * a.part_rows + row]);
+          v[e][p] = __ldcg(
+              reinterpret_cast<const float4 *>(a.part + s * per + (size_t)row * D + c * 4));
+          if (p0 + p >= np) x[e][p] = make_float2(-INFINITY, 0.f);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float top = m[e];
+#pragma unroll
+        for (int p = 0; p < P; ++p) top = fmaxf(top, x[e][p].x);
+        const float use = top == -INFINITY ? 0.f : top, corr = exp2f(m[e] - use);
+        m[e] = top;
+        l[e] *= corr;
+        acc[e].x *= corr;
+        acc[e].y *= corr;
+        acc[e].z *= corr;
+        acc[e].w *= corr;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const float f = exp2f(x[e][p].x - use);
+          l[e] += x[e][p].y * f;
+          acc[e].x += v[e][p].x * f;
+          acc[e].y += v[e][p].y * f;
+          acc[e].z += v[e][p].z * f;
+          acc[e].w += v[e][p].w * f;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = i0 + e * nt;
+      if (i >= total) break;
+      const size_t o = at(row0 + i / (D / 4));
+      const int c = i % (D / 4);
+      const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
+      alignas(16) T r[4] = {DT<T>::from_f(acc[e].x * inv), DT<T>::from_f(acc[e].y * inv),
+                DT<T>::from_f(acc[e].z * inv), DT<T>::from_f(acc[e].w * inv)};
+      using Vec = typename std::conditional<sizeof(T) == 4, float4, uint2>::type;
+      *reinterpret_cast<Vec *>(out + o * D + c * 4) = *reinterpret_cast<const Vec *>(r);
+      if (a.lse && c == 0)
+        a.lse[o] = l[e] > 0.f ? (m[e] + log2f(l[e])) * 0.69314718055994531f : -INFINITY;
+    }
+  }
 }
 
 }  // namespace sd

@@ -7,8 +7,8 @@
 // one (sequence, KV head) and a piece of its key tiles.  Each tile of 64 keys
 // is copied into shared memory, K for S = Q K^T and V for O += P V
 // in turn, the next tile's K arriving while V is used and the other way round.
-// Thread (ty, tx) holds rows ty*4 .. +3 and keys tx + TX*j of S, then columns
-// of O; a row's TX threads are in one warp, so its maximum and sum are warp
+// Thread (ty, tx) holds rows ty*RT .. and keys tx + TX*j of S, then columns of
+// O; a row's TX threads are in one warp, so its maximum and sum are warp
 // shuffles.  A piece of a cut range writes (O, m, l) to its slot; the last
 // piece of the block to arrive merges them in piece order.
 #include "paged.h"
@@ -22,13 +22,13 @@ constexpr int kKT = 64;  // keys per tile
 template <int D, int RB>
 struct SimtCfg {
   static constexpr int TX = RB == 16 ? 32 : 16;
-  static constexpr int kThreads = RB / 4 * TX;
+  static constexpr int RT = RB == 16 ? 4 : 8;  // rows per thread
+  static constexpr int kThreads = RB / RT * TX;
   static constexpr int NK = kKT / TX;      // keys per thread
   static constexpr int NC = D / TX;        // columns per thread
-  static constexpr int QS = D + 4;         // row strides, in floats
-  static constexpr int KS = D + 4;
-  static constexpr int PS = kKT + 4;
-  static constexpr int kFloats = RB * QS + 2 * kKT * KS + RB * PS;
+  static constexpr int PS = kKT;           // row stride of P, in floats
+  static constexpr int kBlocks = RB == 16 ? 2 : D == 64 ? 3 : 2;  // per SM: shared memory's limit
+  static constexpr int kFloats = RB * D + 2 * kKT * D + RB * PS;
   static constexpr int kSmem = kFloats * 4 + 64 + kKT;  // + the claimed item, key flags
   static constexpr int VEC = NC >= 4 ? 4 : NC;  // columns of V read at once
 };
@@ -41,8 +41,9 @@ __device__ __forceinline__ void cp16(void *dst, const void *src, bool pred) {
 
 // keys [key0, key0 + 64) of the sequence, those in [0, limit) that any row of
 // the block sees (j >= low or j < sinks), into dst as fp32 rows; zeros for
-// the others and for pages outside the pool.  kok (nullable): which were read.
-template <int D, int KS, int THREADS>
+// the others and for pages outside the pool.  SWIZZLE: 16-byte pieces permuted by
+// row, so that a column of 8 rows is free of bank conflicts.  kok (nullable): which were read.
+template <int D, bool SWIZZLE, int THREADS>
 __device__ __forceinline__ void load_tile(float *dst, unsigned char *kok, const float *cache,
                                           const PgArgs &a, const int *table, int h, int key0,
                                           int limit, int low) {
@@ -60,18 +61,19 @@ __device__ __forceinline__ void load_tile(float *dst, unsigned char *kok, const 
       else if (c == 0) raise_flag(a.status, FLAG_INDEX);
     }
     if (kok && c == 0) kok[r] = ok;
-    cp16(dst + r * KS + c * PER, cache + off, ok);
+    cp16(dst + r * D + (SWIZZLE ? c ^ (r & 7) : c) * PER, cache + off, ok);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 template <int D, int RB>
-__global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kernel(const PgArgs a) {
+__global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads, SimtCfg<D, RB>::kBlocks)
+    paged_attn_simt_kernel(const PgArgs a) {
   using C = SimtCfg<D, RB>;
-  constexpr int TX = C::TX, NK = C::NK, NC = C::NC, QS = C::QS, KS = C::KS, PS = C::PS;
+  constexpr int TX = C::TX, RT = C::RT, NK = C::NK, NC = C::NC, PS = C::PS;
   constexpr int THREADS = C::kThreads;
   extern __shared__ float sm[];
-  float *Qs = sm, *Ks = Qs + RB * QS, *Vs = Ks + kKT * KS, *Ps = Vs + kKT * KS;
+  float *Qs = sm, *Ks = Qs + RB * D, *Vs = Ks + kKT * D, *Ps = Vs + kKT * D;
   int *box = reinterpret_cast<int *>(Ps + RB * PS);
   unsigned char *kok = reinterpret_cast<unsigned char *>(box + 16);
   const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
@@ -111,46 +113,46 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
         const float *src = q + (size_t)(row0 + t0 + a.by_G(r)) * a.q_stride + (h * G + r - a.by_G(r) * G) * D + c * 4;
         v = *reinterpret_cast<const float4 *>(src);
       }
-      *reinterpret_cast<float4 *>(Qs + r * QS + c * 4) = v;
+      *reinterpret_cast<float4 *>(Qs + r * D + c * 4) = v;
     }
-    float m[4], l[4], o[4][NC];
+    float m[RT], l[RT], o[RT][NC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RT; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
     }
-    int pos[4], lowr[4];
+    int pos[RT], lowr[RT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i;
+    for (int i = 0; i < RT; ++i) {
+      const int r = ty * RT + i;
       pos[i] = r < rows ? p_first + a.by_G(r) : -1;
       lowr[i] = pg_window_low(pos[i], a.window);
     }
     if (u0 < u1)
-      load_tile<D, KS, THREADS>(Ks, kok, K, a, table, h, tiles.tile(u0) * kKT, limit, low);
+      load_tile<D, true, THREADS>(Ks, kok, K, a, table, h, tiles.tile(u0) * kKT, limit, low);
     for (int u = u0; u < u1; ++u) {
       const int key0 = tiles.tile(u) * kKT;
-      load_tile<D, KS, THREADS>(Vs, nullptr, V, a, table, h, key0, limit, low);
+      load_tile<D, false, THREADS>(Vs, nullptr, V, a, table, h, key0, limit, low);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
-      float s[4][NK];
+      float s[RT][NK];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < NK; ++j) s[i][j] = 0.f;
 #pragma unroll 4
       for (int k = 0; k < D; k += 4) {
-        float4 qv[4], kv4[NK];
+        float4 qv[RT], kv4[NK];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          qv[i] = *reinterpret_cast<const float4 *>(Qs + (ty * 4 + i) * QS + k);
+        for (int i = 0; i < RT; ++i)
+          qv[i] = *reinterpret_cast<const float4 *>(Qs + (ty * RT + i) * D + k);
 #pragma unroll
         for (int j = 0; j < NK; ++j)
-          kv4[j] = *reinterpret_cast<const float4 *>(Ks + (tx + TX * j) * KS + k);
+          kv4[j] = *reinterpret_cast<const float4 *>(Ks + (tx + TX * j) * D + (k ^ ((tx & 7) << 2)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
           for (int j = 0; j < NK; ++j) {
             s[i][j] = fmaf(qv[i].x, kv4[j].x, s[i][j]);
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
           }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < RT; ++i) {
         float mx = m[i];
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
         for (int j = 0; j < NK; ++j) {
           const float p = exp2f(s[i][j] - use);
           sum += p;
-          Ps[(ty * 4 + i) * PS + tx + TX * j] = p;
+          Ps[(ty * RT + i) * PS + tx + TX * j] = p;
         }
         l[i] = l[i] * corr + sum;
 #pragma unroll
@@ -188,28 +190,28 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
       }
       __syncthreads();  // K is used up, P complete
       if (u + 1 < u1)
-        load_tile<D, KS, THREADS>(Ks, kok, K, a, table, h, tiles.tile(u + 1) * kKT, limit, low);
+        load_tile<D, true, THREADS>(Ks, kok, K, a, table, h, tiles.tile(u + 1) * kKT, limit, low);
       else
         asm volatile("cp.async.commit_group;" ::: "memory");
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();  // V has landed
 #pragma unroll 2
       for (int k = 0; k < kKT; k += 4) {
-        float4 pv[4];
+        float4 pv[RT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          pv[i] = *reinterpret_cast<const float4 *>(Ps + (ty * 4 + i) * PS + k);
+        for (int i = 0; i < RT; ++i)
+          pv[i] = *reinterpret_cast<const float4 *>(Ps + (ty * RT + i) * PS + k);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           float v[NC];
 #pragma unroll
           for (int c = 0; c < NC; c += C::VEC) {
-            const float *src = Vs + (k + kk) * KS + (c / C::VEC) * (TX * C::VEC) + tx * C::VEC;
+            const float *src = Vs + (k + kk) * D + (c / C::VEC) * (TX * C::VEC) + tx * C::VEC;
 #pragma unroll
             for (int e = 0; e < C::VEC; ++e) v[c + e] = src[e];
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < RT; ++i) {
             const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
 #pragma unroll
             for (int c = 0; c < NC; ++c) o[i][c] = fmaf(p, v[c], o[i][c]);
@@ -221,14 +223,14 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     // the row's sum over its threads
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int w = TX / 2; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
 
     if (sq.np == 1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
+      for (int i = 0; i < RT; ++i) {
+        const int r = ty * RT + i;
         if (r >= rows) continue;
         const size_t tok = (size_t)(row0 + t0 + a.by_G(r)), hq = h * G + r - a.by_G(r) * G;
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
@@ -247,8 +249,8 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
       float2 *ml = reinterpret_cast<float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
       const size_t mine = first + (size_t)piece * a.Hkv + h;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
+      for (int i = 0; i < RT; ++i) {
+        const int r = ty * RT + i;
         if (r >= rows) continue;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -265,31 +267,11 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads) paged_attn_simt_kern
       __syncthreads();
       if (last) {
         __threadfence();
-        for (int r = tid / 32; r < rows; r += THREADS / 32) {
-          const int lane = tid & 31;
-          float mm = -INFINITY;
-          for (int p = 0; p < sq.np; ++p)
-            mm = fmaxf(mm, __ldcg(&ml[(first + (size_t)p * a.Hkv + h) * a.part_rows + r].x));
-          const float use = mm == -INFINITY ? 0.f : mm;
-          float acc[D / 32] = {}, ll = 0.f;
-          for (int p = 0; p < sq.np; ++p) {
-            const size_t s = first + (size_t)p * a.Hkv + h;
-            const float2 e = __ldcg(&ml[s * a.part_rows + r]);
-            const float w = exp2f(e.x - use);
-            ll += e.y * w;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c)
-              acc[c] += __ldcg(&a.part[s * per + (size_t)r * D + c * 32 + lane]) * w;
-          }
-          const float inv = ll > 0.f ? 1.f / ll : 0.f;
-          const size_t tok = (size_t)(row0 + t0 + a.by_G(r)), hq = h * G + r - a.by_G(r) * G;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-            out[(tok * a.Hq + hq) * D + c * 32 + lane] = acc[c] * inv;
-          if (a.lse && lane == 0)
-            a.lse[tok * a.Hq + hq] =
-                ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
-        }
+        pg_merge<D>(a, first + h, sq.np, 0, rows, tid, THREADS,
+                    [&](int r) {
+                      return (size_t)(row0 + t0 + a.by_G(r)) * a.Hq + h * G + r - a.by_G(r) * G;
+                    },
+                    out);
       }
     }
     __syncthreads();

@@ -723,35 +723,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
         sm->last[t] = atomicAdd(&a.arrive[first + (size_t)t * a.Hkv], 1u) == (uint32_t)(I.np - 1);
       if (!(ok = wg_sync())) break;
       if (sm->last[t]) {
-        // the block's last piece to arrive merges them all, in order; a warp per row
+        // the block's last piece to arrive merges them all
         __threadfence();
-        const int rows_here = min(I.rows - t * tile_rows, tile_rows);
-        for (int rr = warp & 3; rr < rows_here; rr += 4) {
-          const int row = t * tile_rows + rr;
-          float mm = -INFINITY;
-          for (int p = 0; p < I.np; ++p)
-            mm = fmaxf(mm, __ldcg(&ml[(first + (size_t)p * a.Hkv) * a.part_rows + row].x));
-          const float us = mm == -INFINITY ? 0.f : mm;
-          float acc[D / 32] = {}, ll = 0.f;
-          for (int p = 0; p < I.np; ++p) {
-            const size_t sl = first + (size_t)p * a.Hkv;
-            const float2 e = __ldcg(&ml[sl * a.part_rows + row]);
-            const float f = exp2f(e.x - us);
-            ll += e.y * f;
-            if (f > 0.f) {
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c)
-                acc[c] += __ldcg(&a.part[sl * per + (size_t)row * D + c * 32 + lane]) * f;
-            }
-          }
-          const float iv = ll > 0.f ? 1.f / ll : 0.f;
-          const size_t o = (size_t)(I.row0 + I.t0 + a.by_G(row)) * a.Hq + I.h * G + row - a.by_G(row) * G;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-            out[o * D + c * 32 + lane] = __float2bfloat16_rn(acc[c] * iv);
-          if (a.lse && lane == 0)
-            a.lse[o] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
-        }
+        pg_merge<D>(a, first, I.np, t * tile_rows, min(I.rows - t * tile_rows, tile_rows), r, 128,
+                    [&](int row) {
+                      return (size_t)(I.row0 + I.t0 + a.by_G(row)) * a.Hq + I.h * G + row -
+                             a.by_G(row) * G;
+                    },
+                    out);
       }
       if (!(ok = wg_sync())) break;  // sm->last is read before the next item's
       done();

@@ -13,7 +13,7 @@
 // piece + a fixed part for starting a piece and, when cut, for writing and
 // merging its partial).  The cheapest whose partials fit the workspace wins;
 // ties go to fewer pieces.  One CTA; latency bound (it also resets the call's
-// counters, so nothing in the workspace has to be zero before a call).
+// counters, so nothing of them has to be zero before a call).
 #include "paged.h"
 #include "paged.cuh"
 
@@ -29,64 +29,62 @@ constexpr int kPieceCost = 2, kCutCost = 8;
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// blocks of a sequence's rows, and the most key tiles that one of them reads
+__device__ __forceinline__ int sc_blocks(const PgArgs &a, int b, int TB, int KT, int *u,
+                                         bool report) {
+  int row0, n, kv;
+  *u = 1;
+  if (!pg_lengths(a, b, &row0, &n, &kv)) {
+    if (report) raise_flag(a.status, FLAG_INDEX);
+    return 0;
+  }
+  const int nrb = ceil_div(n, TB);
+  if (nrb > 0) {
+    // the last block sees the most keys; a window bounds every block
+    int x = pg_tiles(kv - n + (nrb - 1) * TB, kv - 1, a.window, a.sinks, KT).units();
+    if (a.window > 0 && nrb > 1)
+      x = min(ceil_div(kv, KT), ceil_div(min(a.sinks, kv), KT) +
+                                    (int)(((long long)a.window + TB - 2) / KT) + 2);
+    *u = max(x, 1);
+  }
+  return nrb;
+}
+
+// Every warp walks the batch itself, so the candidates meet at one barrier.
 __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs a, int TB, int KT,
                                                                     int workers) {
-  __shared__ int s_nrb[kPagedMaxB], s_u[kPagedMaxB];
-  __shared__ int s_max, s_best;
   __shared__ unsigned long long s_cost[kCand];
-  __shared__ int s_w[kScThreads / 32][2], s_carry[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_wait();
   grid_dep_launch();
-  if (tid == 0) {
-    s_max = 1;
-    s_carry[0] = s_carry[1] = 0;
-    a.head->next = 0;
+  if (tid == 0) a.head->next = 0;
+  int umax = 1;
+  for (int b = lane; b < a.B; b += 32) {
+    int u;
+    if (sc_blocks(a, b, TB, KT, &u, warp == 0)) umax = max(umax, u);
   }
-  __syncthreads();
-  int most = 1;
-  for (int b = tid; b < a.B; b += kScThreads) {
-    int row0, n, kv, nrb = 0, u = 1;
-    if (pg_lengths(a, b, &row0, &n, &kv)) {
-      nrb = ceil_div(n, TB);
-      if (nrb > 0) {
-        // the last block sees the most keys; a window bounds every block
-        const PgTiles last = pg_tiles(kv - n + (nrb - 1) * TB, kv - 1, a.window, a.sinks, KT);
-        u = last.units();
-        if (a.window > 0 && nrb > 1)
-          u = min(ceil_div(kv, KT), ceil_div(min(a.sinks, kv), KT) +
-                                        (int)(((long long)a.window + TB - 2) / KT) + 2);
-        u = max(u, 1);
-      }
-    } else {
-      raise_flag(a.status, FLAG_INDEX);
-    }
-    s_nrb[b] = nrb;
-    s_u[b] = u;
-    if (nrb) most = max(most, u);
-  }
-  atomicMax(&s_max, most);
-  __syncthreads();
-  const int umax = s_max;
+  umax = __reduce_max_sync(0xffffffffu, umax);
   {
     // this warp's candidate
     const int C = ceil_div(umax, kPieces[warp]);
     long long pieces = 0, slots = 0;
     int longest = 1, cut = 0;
     for (int b = lane; b < a.B; b += 32) {
-      const int np = ceil_div(s_u[b], C);
-      if (!s_nrb[b]) continue;
-      pieces += (long long)s_nrb[b] * np;
-      if (np > 1) slots += (long long)s_nrb[b] * np, cut = 1;
-      longest = max(longest, ceil_div(s_u[b], np));
+      int u;
+      const int nrb = sc_blocks(a, b, TB, KT, &u, false);
+      if (!nrb) continue;
+      const int np = ceil_div(u, C);
+      pieces += (long long)nrb * np;
+      if (np > 1) slots += (long long)nrb * np, cut = 1;
+      longest = max(longest, ceil_div(u, np));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
       slots += __shfl_xor_sync(0xffffffffu, slots, o);
-      longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-      cut |= __shfl_xor_sync(0xffffffffu, cut, o);
     }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    cut = __reduce_or_sync(0xffffffffu, cut);
     if (lane == 0) {
       const unsigned long long waves =
           ((unsigned long long)pieces * a.Hkv + workers - 1) / workers;
@@ -96,22 +94,31 @@ __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    int best = 0;  // one piece needs no slot: always possible
-    for (int i = 1; i < kCand; ++i)
-      if (s_cost[i] < s_cost[best]) best = i;
-    s_best = ceil_div(umax, kPieces[best]);
+  if (warp > 0) {
+    for (int i = tid - 32; i < a.slot_cap * a.Hkv; i += kScThreads - 32) a.arrive[i] = 0u;
+    return;
   }
-  __syncthreads();
-  const int C = s_best;
-  // exclusive prefix sums of items and slots, kScThreads sequences at a time
-  for (int b0 = 0; b0 < a.B; b0 += kScThreads) {
-    const int b = b0 + tid;
+  // the cheapest (one piece needs no slot: always possible)
+  unsigned long long cost = s_cost[lane];
+  int best = lane;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long c = __shfl_xor_sync(0xffffffffu, cost, o);
+    const int i = __shfl_xor_sync(0xffffffffu, best, o);
+    if (c < cost || (c == cost && i < best)) cost = c, best = i;
+  }
+  const int C = ceil_div(umax, kPieces[best]);
+  // exclusive prefix sums of items and slots
+  int bx = 0, by = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
     int np = 1, len = 1, items = 0, slots = 0;
     if (b < a.B) {
-      np = ceil_div(s_u[b], C);
-      len = ceil_div(s_u[b], np);
-      items = s_nrb[b] * np;
+      int u;
+      const int nrb = sc_blocks(a, b, TB, KT, &u, false);
+      np = ceil_div(u, C);
+      len = ceil_div(u, np);
+      items = nrb * np;
       slots = np > 1 ? items : 0;
     }
     int x = items, y = slots;
@@ -120,17 +127,11 @@ __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs
       const int px = __shfl_up_sync(0xffffffffu, x, o), py = __shfl_up_sync(0xffffffffu, y, o);
       if (lane >= o) x += px, y += py;
     }
-    if (lane == 31) s_w[warp][0] = x, s_w[warp][1] = y;
-    __syncthreads();
-    int bx = s_carry[0], by = s_carry[1];
-    for (int w = 0; w < warp; ++w) bx += s_w[w][0], by += s_w[w][1];
     if (b < a.B) a.seqs[b] = PgSeq{bx + x - items, by + y - slots, np, len};
-    __syncthreads();
-    if (tid == kScThreads - 1) s_carry[0] = bx + x, s_carry[1] = by + y;
-    __syncthreads();
+    bx += __shfl_sync(0xffffffffu, x, 31);
+    by += __shfl_sync(0xffffffffu, y, 31);
   }
-  if (tid == 0) a.seqs[a.B] = PgSeq{s_carry[0], s_carry[1], 1, 1};
-  for (int i = tid; i < a.slot_cap * a.Hkv; i += kScThreads) a.arrive[i] = 0u;
+  if (lane == 0) a.seqs[a.B] = PgSeq{bx, by, 1, 1};
 }
 
 }  // namespace
