@@ -372,7 +372,7 @@ sparse_status_t sparse_louver_decode_step(const sparse_shape_t *shape, int32_t L
  *
  * page_size is a multiple of 16, or max_blocks is 1; B <= 4096; T <= 2^24;
  * num_pages * page_size < 2^31; max_blocks * page_size <= 2^30; B * Hkv *
- * (max_blocks * page_size / 64 + 32) < 2^31; d, dtype and Hq / Hkv as
+ * (max_blocks * page_size / 32 + 32) < 2^31; d, dtype and Hq / Hkv as
  * everywhere. */
 typedef struct {
   int32_t B;          /* sequences */

@@ -41,8 +41,8 @@ sparse_status_t check_paged(const sparse_paged_shape_t *p, PagedShape *s) {
   if ((long long)s->pages * s->page > 0x7fffffffll ||
       (long long)s->pages * s->Hkv > 0x7fffffffll ||
       (long long)s->blocks * s->page > (1ll << 30) || s->T > (1 << 24) ||
-      // the 64-key tiles that the longest batch has, in 31 bits
-      (long long)s->B * s->Hkv * ((long long)s->blocks * s->page / 64 + 32) > 0x7fffffffll)
+      // the 32-key tiles that the longest batch has, in 31 bits
+      (long long)s->B * s->Hkv * ((long long)s->blocks * s->page / 32 + 32) > 0x7fffffffll)
     return SPARSE_ERR_UNSUPPORTED;
   if (s->max_new == 0 || s->max_new > s->T) s->max_new = s->T;
   return SPARSE_OK;
@@ -193,9 +193,12 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
   a.slot_cap = l.slot_cap;
   a.part_rows = l.part_rows;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (s.dtype == SPARSE_DTYPE_F32) return sd::status_of(sd::launch_paged_attn_simt(s, a, st));
-  return sd::status_of(s.max_new * s.G() <= 16 ? sd::launch_paged_decode(s, a, st)
-                                               : sd::launch_paged_chunk(s, a, st));
+  // few rows per cache row: bound by memory; many: by arithmetic
+  const bool few = s.max_new * s.G() <= 16;
+  if (s.dtype == SPARSE_DTYPE_F32)
+    return sd::status_of(few ? sd::launch_paged_decode_f32(s, a, st)
+                             : sd::launch_paged_attn_simt(s, a, st));
+  return sd::status_of(few ? sd::launch_paged_decode(s, a, st) : sd::launch_paged_chunk(s, a, st));
 }
 
 }  // extern "C"

@@ -21,13 +21,13 @@ constexpr int kKT = 64;  // keys per tile
 
 template <int D, int RB>
 struct SimtCfg {
-  static constexpr int TX = RB == 16 ? 32 : 16;
-  static constexpr int RT = RB == 16 ? 4 : 8;  // rows per thread
+  static constexpr int TX = 16;
+  static constexpr int RT = 8;             // rows per thread
   static constexpr int kThreads = RB / RT * TX;
   static constexpr int NK = kKT / TX;      // keys per thread
   static constexpr int NC = D / TX;        // columns per thread
   static constexpr int PS = kKT;           // row stride of P, in floats
-  static constexpr int kBlocks = RB == 16 ? 2 : D == 64 ? 3 : 2;  // per SM: shared memory's limit
+  static constexpr int kBlocks = D == 64 ? 3 : 2;  // per SM: shared memory's limit
   static constexpr int kFloats = RB * D + 2 * kKT * D + RB * PS;
   static constexpr int kSmem = kFloats * 4 + 64 + kKT;  // + the claimed item, key flags
   static constexpr int VEC = NC >= 4 ? 4 : NC;  // columns of V read at once
@@ -305,16 +305,10 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int D>
-cudaError_t pick(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
-  // up to 16 rows per (sequence, KV head): the cache is read once, memory bound
-  return s.max_new * s.G() <= 16 ? run<D, 16>(s, a, st) : run<D, 64>(s, a, st);
-}
-
 }  // namespace
 
 cudaError_t launch_paged_attn_simt(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
-  return s.d == 64 ? pick<64>(s, a, st) : pick<128>(s, a, st);
+  return s.d == 64 ? run<64, 64>(s, a, st) : run<128, 64>(s, a, st);
 }
 
 }  // namespace sd

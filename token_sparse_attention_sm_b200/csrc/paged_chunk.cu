@@ -753,12 +753,12 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   auto kern = paged_chunk_kernel<D>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const PgTile tile = pg_tile(s.page, s.blocks, D, kChKeys);
+  const PgTile tile = pg_tile(s.page, s.blocks, D * 2, kChKeys);
   const int TPT = 128 / s.G();
   CUtensorMap mq, mk, mv;
   e = pg_query_map(&mq, a.q, D, s.Hq, s.T, a.q_stride, s.G(), TPT);
-  if (e == cudaSuccess) e = pg_cache_map(&mk, a.K, D, s.page, (long long)s.pages * s.Hkv, tile);
-  if (e == cudaSuccess) e = pg_cache_map(&mv, a.V, D, s.page, (long long)s.pages * s.Hkv, tile);
+  if (e == cudaSuccess) e = pg_cache_map(&mk, a.K, s, tile);
+  if (e == cudaSuccess) e = pg_cache_map(&mv, a.V, s, tile);
   if (e != cudaSuccess) return e;
   if ((e = launch_paged_schedule(s, a, 2 * TPT, kChKeys, di.sm_count, st)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -1,10 +1,10 @@
-// paged_tma.h -- tensor maps over a paged cache (bf16).  One copy brings the
+// paged_tma.h -- tensor maps over a paged cache.  One copy brings the
 // part of a key tile that lies in one page, all d columns, in 128-byte rows of
-// 64 elements, 128-byte swizzled.  Two shared-memory layouts:
-//  * the whole tile is one part: [64-column block][key][128 B];
-//  * several parts: [8 keys][64-column block][key of the 8][128 B], so that the
+// 64 bf16 or 32 fp32 elements, 128-byte swizzled.  Two shared-memory layouts:
+//  * the whole tile is one part: [column block][key][128 B];
+//  * several parts: [8 keys][column block][key of the 8][128 B], so that the
 //    parts, one after another, make the same uniform layout.
-// (One copy per part and 64-column block, as a plain 2-D tile would need, is
+// (One copy per part and column block, as a plain 2-D tile would need, is
 // bound by issuing the copies when pages are short: 16-token pages at d = 128
 // streamed at 5.2 TB/s, 32-token ones at 6.8.)  Coordinates past the pool, and
 // tokens past a single page's end, read zeros.
@@ -28,21 +28,22 @@ inline int pg_part_rows(int page, int blocks, int KT) {
 }
 
 // Byte strides of a tile's layout in shared memory: between groups of 8 keys,
-// between 64-column blocks.
+// between column blocks.
 struct PgTile {
   int part;  // keys of a part
   int whole; // the tile is one part
   int group, col;
 };
-inline PgTile pg_tile(int page, int blocks, int d, int KT) {
+inline PgTile pg_tile(int page, int blocks, int row_bytes, int KT) {
   const int part = pg_part_rows(page, blocks, KT);
   if (part == KT) return PgTile{part, 1, 1024, KT * 128};
-  return PgTile{part, 0, d / 64 * 1024, 1024};
+  return PgTile{part, 0, row_bytes / 128 * 1024, 1024};
 }
 
-cudaError_t pg_cache_map(CUtensorMap *map, const void *cache, int d, int page,
-                         long long pages_heads, const PgTile &t);
-// q [T, Hq, d] (tokens q_stride elements apart) as (element, head, token),
+struct PagedShape;
+cudaError_t pg_cache_map(CUtensorMap *map, const void *cache, const PagedShape &s,
+                         const PgTile &t);
+// q [T, Hq, d] in bf16 (tokens q_stride elements apart) as (element, head, token),
 // tiles of 64 elements x `heads` x `tokens`.
 cudaError_t pg_query_map(CUtensorMap *map, const void *q, int d, int Hq, int T,
                          long long q_stride, int heads, int tokens);
