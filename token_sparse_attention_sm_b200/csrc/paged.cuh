@@ -72,6 +72,36 @@ struct PgArgs {
   int part_rows;
 };
 
+// pairs of fp32 values in one 64-bit register, and packed arithmetic on them
+__device__ __forceinline__ uint64_t pg_u2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pg_f2(float lo, float hi) {
+  return pg_u2(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ void pg_split(uint64_t x, float *lo, float *hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(x));
+  *lo = __uint_as_float(a);
+  *hi = __uint_as_float(b);
+}
+__device__ __forceinline__ uint64_t pg_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pg_mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pg_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // 2^x by the hardware approximation (relative error about 2^-22; results
 // below 2^-126 flush to zero, which a softmax weight does not notice).
 __device__ __forceinline__ float pg_exp2(float x) {
@@ -145,10 +175,11 @@ __device__ __forceinline__ int pg_find(const PgSeq *seqs, int B, int x, PgSeq *o
 // the others follow a.Hkv apart; at(row) is a row's place in out [T, Hq].
 // Several elements and pieces are loaded together: row by row, one piece after
 // another, this was a tail of 80 us (13 pieces of 64 rows).
-template <int D, typename T, typename At>
+// E: elements a thread has in flight.
+template <int D, int E, typename T, typename At>
 __device__ __forceinline__ void pg_merge(const PgArgs &a, size_t slot0, int np, int row0, int rows,
                                          int tid, int nt, At at, T *out) {
-  constexpr int E = 4, P = 4;  // elements of a thread, pieces at a time
+  constexpr int P = 4;  // pieces at a time
   const size_t per = (size_t)a.part_rows * D;
   const float2 *ml = reinterpret_cast<const float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
   const int total = rows * (D / 4);

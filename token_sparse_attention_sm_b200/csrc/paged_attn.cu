@@ -30,7 +30,7 @@ struct SimtCfg {
   static constexpr int kBlocks = D == 64 ? 3 : 2;  // per SM: shared memory's limit
   static constexpr int kFloats = RB * D + 2 * kKT * D + RB * PS;
   static constexpr int kSmem = kFloats * 4 + 64 + kKT;  // + the claimed item, key flags
-  static constexpr int VEC = NC >= 4 ? 4 : NC;  // columns of V read at once
+  static_assert(NC % 4 == 0, "16-byte reads of V");
 };
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool pred) {
@@ -115,13 +115,14 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads, SimtCfg<D, RB>::kBlo
       }
       *reinterpret_cast<float4 *>(Qs + r * D + c * 4) = v;
     }
-    float m[RT], l[RT], o[RT][NC];
+    float m[RT], l[RT];
+    uint64_t o[RT][NC / 2];  // pairs of columns
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
+      for (int c = 0; c < NC / 2; ++c) o[i][c] = 0ull;
     }
     int pos[RT], lowr[RT];
 #pragma unroll
@@ -137,30 +138,39 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads, SimtCfg<D, RB>::kBlo
       load_tile<D, false, THREADS>(Vs, nullptr, V, a, table, h, key0, limit, low);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
-      float s[RT][NK];
+      // S, even and odd elements of the rows in the two halves of a pair
+      uint64_t s2[RT][NK];
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int j = 0; j < NK; ++j) s[i][j] = 0.f;
+        for (int j = 0; j < NK; ++j) s2[i][j] = 0ull;
 #pragma unroll 4
       for (int k = 0; k < D; k += 4) {
-        float4 qv[RT], kv4[NK];
+        ulonglong2 qv[RT], kv4[NK];
 #pragma unroll
         for (int i = 0; i < RT; ++i)
-          qv[i] = *reinterpret_cast<const float4 *>(Qs + (ty * RT + i) * D + k);
+          qv[i] = *reinterpret_cast<const ulonglong2 *>(Qs + (ty * RT + i) * D + k);
 #pragma unroll
         for (int j = 0; j < NK; ++j)
-          kv4[j] = *reinterpret_cast<const float4 *>(Ks + (tx + TX * j) * D + (k ^ ((tx & 7) << 2)));
+          kv4[j] = *reinterpret_cast<const ulonglong2 *>(Ks + (tx + TX * j) * D +
+                                                         (k ^ ((tx & 7) << 2)));
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
           for (int j = 0; j < NK; ++j) {
-            s[i][j] = fmaf(qv[i].x, kv4[j].x, s[i][j]);
-            s[i][j] = fmaf(qv[i].y, kv4[j].y, s[i][j]);
-            s[i][j] = fmaf(qv[i].z, kv4[j].z, s[i][j]);
-            s[i][j] = fmaf(qv[i].w, kv4[j].w, s[i][j]);
+            s2[i][j] = pg_fma2(qv[i].x, kv4[j].x, s2[i][j]);
+            s2[i][j] = pg_fma2(qv[i].y, kv4[j].y, s2[i][j]);
           }
       }
+      float s[RT][NK];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+          float even, odd;
+          pg_split(s2[i][j], &even, &odd);
+          s[i][j] = even + odd;
+        }
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         float mx = m[i];
@@ -180,13 +190,13 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads, SimtCfg<D, RB>::kBlo
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
-          const float p = exp2f(s[i][j] - use);
+          const float p = pg_exp2(s[i][j] - use);
           sum += p;
           Ps[(ty * RT + i) * PS + tx + TX * j] = p;
         }
         l[i] = l[i] * corr + sum;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) o[i][c] *= corr;
+        for (int c = 0; c < NC / 2; ++c) o[i][c] = pg_mul2(o[i][c], pg_f2(corr, corr));
       }
       __syncthreads();  // K is used up, P complete
       if (u + 1 < u1)
@@ -203,18 +213,20 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads, SimtCfg<D, RB>::kBlo
           pv[i] = *reinterpret_cast<const float4 *>(Ps + (ty * RT + i) * PS + k);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          float v[NC];
+          uint64_t v[NC / 2];
 #pragma unroll
-          for (int c = 0; c < NC; c += C::VEC) {
-            const float *src = Vs + (k + kk) * D + (c / C::VEC) * (TX * C::VEC) + tx * C::VEC;
-#pragma unroll
-            for (int e = 0; e < C::VEC; ++e) v[c + e] = src[e];
+          for (int c = 0; c < NC; c += 4) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(
+                Vs + (k + kk) * D + (c / 4) * (TX * 4) + tx * 4);
+            v[c / 2] = x.x;
+            v[c / 2 + 1] = x.y;
           }
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
             const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
+            const uint64_t pp = pg_f2(p, p);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) o[i][c] = fmaf(p, v[c], o[i][c]);
+            for (int c = 0; c < NC / 2; ++c) o[i][c] = pg_fma2(pp, v[c], o[i][c]);
           }
         }
       }
@@ -235,9 +247,12 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads, SimtCfg<D, RB>::kBlo
         const size_t tok = (size_t)(row0 + t0 + a.by_G(r)), hq = h * G + r - a.by_G(r) * G;
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int col = (c / C::VEC) * (TX * C::VEC) + tx * C::VEC + c % C::VEC;
-          out[(tok * a.Hq + hq) * D + col] = o[i][c] * inv;
+        for (int c = 0; c < NC; c += 4) {
+          ulonglong2 x;
+          x.x = pg_mul2(o[i][c / 2], pg_f2(inv, inv));
+          x.y = pg_mul2(o[i][c / 2 + 1], pg_f2(inv, inv));
+          *reinterpret_cast<ulonglong2 *>(out + (tok * a.Hq + hq) * D + (c / 4) * (TX * 4) +
+                                          tx * 4) = x;
         }
         if (a.lse && tx == 0)
           a.lse[tok * a.Hq + hq] =
@@ -253,9 +268,12 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads, SimtCfg<D, RB>::kBlo
         const int r = ty * RT + i;
         if (r >= rows) continue;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int col = (c / C::VEC) * (TX * C::VEC) + tx * C::VEC + c % C::VEC;
-          a.part[mine * per + (size_t)r * D + col] = o[i][c];
+        for (int c = 0; c < NC; c += 4) {
+          ulonglong2 x;
+          x.x = o[i][c / 2];
+          x.y = o[i][c / 2 + 1];
+          *reinterpret_cast<ulonglong2 *>(a.part + mine * per + (size_t)r * D +
+                                          (c / 4) * (TX * 4) + tx * 4) = x;
         }
         if (tx == 0) ml[mine * a.part_rows + r] = make_float2(m[i], l[i]);
       }
@@ -267,7 +285,7 @@ __global__ void __launch_bounds__(SimtCfg<D, RB>::kThreads, SimtCfg<D, RB>::kBlo
       __syncthreads();
       if (last) {
         __threadfence();
-        pg_merge<D>(a, first + h, sq.np, 0, rows, tid, THREADS,
+        pg_merge<D, 4>(a, first + h, sq.np, 0, rows, tid, THREADS,
                     [&](int r) {
                       return (size_t)(row0 + t0 + a.by_G(r)) * a.Hq + h * G + r - a.by_G(r) * G;
                     },

@@ -44,8 +44,8 @@ constexpr int kChKeys = 128;
 constexpr int kChSoftWarps = 8;
 constexpr int kChThreads = 384;  // three warpgroups: two of softmax warps; MMA and copies
 // registers a thread: 168 at launch, moved from the third warpgroup to the
-// softmax ones (2 * 128 * 224 + 128 * 56 = 384 * 168)
-constexpr int kChSoftRegs = 224, kChOtherRegs = 56;
+// softmax ones (2 * 128 * 216 + 128 * 72 = 384 * 168)
+constexpr int kChSoftRegs = 216, kChOtherRegs = 72;
 constexpr int kChMmaWarp = kChSoftWarps, kChTmaWarp = kChSoftWarps + 2;  // row tiles' MMA; K, V
 constexpr float kChLag = 8.f;  // log2 units the maximum may run ahead of its reference
 
@@ -150,31 +150,6 @@ __device__ __forceinline__ void ch_tma(uint32_t dst, const CUtensorMap *map, int
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
-}
-// pairs of fp32 values in one 64-bit register, and packed arithmetic on them
-__device__ __forceinline__ uint64_t ch_u2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t ch_f2(float lo, float hi) {
-  return ch_u2(__float_as_uint(lo), __float_as_uint(hi));
-}
-__device__ __forceinline__ void ch_split(uint64_t x, float *lo, float *hi) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(x));
-  *lo = __uint_as_float(a);
-  *hi = __uint_as_float(b);
-}
-__device__ __forceinline__ uint64_t ch_fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t ch_add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 // one lane of a converged warp, always the same
 __device__ __forceinline__ bool ch_elect() {
@@ -587,20 +562,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
                            (key0 >= low_last || key0 + kChKeys <= a.sinks) && good == all_ok;
         uint32_t s[128], p[32];
         uint64_t sum2[2];
-        const uint64_t scale2 = ch_f2(a.scale_log2, a.scale_log2);
+        const uint64_t scale2 = pg_f2(a.scale_log2, a.scale_log2);
         // weights of keys 64 c .. 64 c + 63 against the reference m
         auto weights = [&](int c, bool fresh) {
           const float use = m == -INFINITY ? 0.f : m;
-          const uint64_t neg2 = ch_f2(-use, -use);
+          const uint64_t neg2 = pg_f2(-use, -use);
           if (fresh) sum2[0] = sum2[1] = 0ull;  // pairs of zeros
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int k = c * 64 + i * 2;
             float p0, p1;
-            ch_split(ch_fma2(ch_u2(s[k], s[k + 1]), scale2, neg2), &p0, &p1);
+            pg_split(pg_fma2(pg_u2(s[k], s[k + 1]), scale2, neg2), &p0, &p1);
             p0 = pg_exp2(p0);
             p1 = pg_exp2(p1);
-            sum2[i & 1] = ch_add2(sum2[i & 1], ch_f2(p0, p1));
+            sum2[i & 1] = pg_add2(sum2[i & 1], pg_f2(p0, p1));
             p[i] = ch_pack(p0, p1);
           }
         };
@@ -660,7 +635,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (lane == 0) mbar_arrive(&sm->p_ready[t][c]);
         }
         float a0, a1;
-        ch_split(ch_add2(sum2[0], sum2[1]), &a0, &a1);
+        pg_split(pg_add2(sum2[0], sum2[1]), &a0, &a1);
         l += a0 + a1;
       }
       if (!ok) break;
@@ -725,7 +700,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       if (sm->last[t]) {
         // the block's last piece to arrive merges them all
         __threadfence();
-        pg_merge<D>(a, first, I.np, t * tile_rows, min(I.rows - t * tile_rows, tile_rows), r, 128,
+        pg_merge<D, 4>(a, first, I.np, t * tile_rows, min(I.rows - t * tile_rows, tile_rows), r, 128,
                     [&](int row) {
                       return (size_t)(I.row0 + I.t0 + a.by_G(row)) * a.Hq + I.h * G + row -
                              a.by_G(row) * G;
