@@ -237,6 +237,72 @@ def test_attn_decode(lib, dtype, page, window, sinks):
 
 @gpu
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,new", [(4, 4, 1), (4, 4, 11), (6, 2, 1), (10, 2, 1), (6, 2, 5),
+                                        (16, 2, 2), (16, 1, 1), (14, 1, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 20)])
+def test_attn_few_rows(lib, dtype, d, Hq, Hkv, new, window, sinks):
+    """Every number of rows up to the 16 of the decode kernels, tokens and
+    groups of heads mixed."""
+    kv = [new, 31, 32, 33, 200, 1000]
+    x = _batch([new, 1, 0, min(new, 2), new, new], kv, Hq, Hkv, d, 16, dtype, seed=Hq + new)
+    _assert_attn(x, sd.paged_attn(*x["args"], window=window, sinks=sinks, max_new=new), window,
+                 sinks)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B", [1000, 4096])
+def test_attn_many_sequences(lib, dtype, B):
+    """Runs over many short caches, some without new tokens, some empty."""
+    new = [0 if i % 7 == 3 else 1 for i in range(B)]
+    kv = [(i * 37) % 90 if i % 11 else 0 for i in range(B)]
+    x = _batch(new, kv, 4, 2, 64, 16, dtype, seed=B)
+    _assert_attn(x, sd.paged_attn(*x["args"], max_new=1))
+    if B == 1000:
+        _assert_attn(x, sd.paged_attn(*x["args"], max_new=40))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_attn_padding_may_hold_anything(lib, dtype):
+    """NaN in the padding rows of q and in the rows between two tokens' heads."""
+    for new in ([1, 1, 1], [30, 1, 45]):
+        x = _batch(new, [50, 20, 90], 8, 2, 64, 16, dtype, seed=3, pad=70, q_pad=8)
+        T = sum(new)
+        q = x["args"][0]
+        q[T:] = float("nan")
+        base = q._base if q._base is not None else q
+        base.view(T + 70, -1)[:, 8 * 64:] = float("nan")
+        out = torch.full(q.shape, 3.0, dtype=dtype, device="cuda")
+        got = sd.paged_attn(*x["args"], max_new=max(new), out=out)
+        _assert_attn(x, got)
+        assert (out[T:] == 3).all()
+
+
+@gpu
+def test_a_workspace_shared_with_the_decode_step(lib):
+    """Ordered calls of both kinds on one workspace leave each other alone."""
+    g = torch.Generator().manual_seed(2)
+    K, V = (torch.randn(1, 2, 5000, 128, generator=g).to(BF16).cuda() for _ in range(2))
+    q = torch.randn(1, 8, 128, generator=g).to(BF16).cuda()
+    ref = sd.decode_step(q, q[None], K, V, k=100)
+    x = _batch([1, 60], [3000, 700], 8, 2, 128, 16, BF16, seed=1)
+    ws = sd.Workspace()
+    for _ in range(3):
+        got = sd.paged_attn(*x["args"], ws=ws)
+        dec = sd.paged_attn(x["args"][0][:1], *x["args"][1:3], x["args"][3][:1].contiguous(),
+                            x["args"][4][:2].contiguous(), x["args"][5][:1].contiguous(),
+                            max_new=1, ws=ws)
+        step = sd.decode_step(q, q[None], K, V, k=100, ws=ws)
+        assert sd.read_device_flags(ws) == 0
+        assert torch.equal(step["idx"], ref["idx"]) and torch.equal(step["out"], ref["out"])
+        _assert_attn(x, got)
+        assert torch.allclose(dec[1], got[1][:1], atol=1e-4)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("new,kv,window,sinks", [
     ([300], [300], 0, 0), ([300], [300], 128, 4), ([257], [1300], 0, 0), ([64], [4000], 0, 0),
     ([513], [900], 200, 129), ([129, 1, 400], [129, 2500, 401], 0, 0), ([9], [3100], 1000, 16),
