@@ -30,9 +30,9 @@ constexpr int kPagedTops = 12;
 cudaError_t launch_paged_decode(const PagedShape &s, const PgArgs &a, cudaStream_t st);
 // bf16, any number of rows (paged_chunk.cu): tcgen05.
 cudaError_t launch_paged_chunk(const PagedShape &s, const PgArgs &a, cudaStream_t st);
-// fp32, at most 16 rows (paged_decode_f32.cu), any number (paged_attn.cu).
+// fp32, at most 16 rows (paged_decode_f32.cu), any number (paged_chunk_f32.cu).
 cudaError_t launch_paged_decode_f32(const PagedShape &s, const PgArgs &a, cudaStream_t st);
-cudaError_t launch_paged_attn_simt(const PagedShape &s, const PgArgs &a, cudaStream_t st);
+cudaError_t launch_paged_chunk_f32(const PagedShape &s, const PgArgs &a, cudaStream_t st);
 // The work items' schedule for row blocks of `tb` tokens, key tiles of `kt`
 // keys and `grid` workers (paged_sched.cu).
 cudaError_t launch_paged_schedule(const PagedShape &s, const PgArgs &a, int tb, int kt, int grid,

@@ -197,7 +197,7 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
   const bool few = s.max_new * s.G() <= 16;
   if (s.dtype == SPARSE_DTYPE_F32)
     return sd::status_of(few ? sd::launch_paged_decode_f32(s, a, st)
-                             : sd::launch_paged_attn_simt(s, a, st));
+                             : sd::launch_paged_chunk_f32(s, a, st));
   return sd::status_of(few ? sd::launch_paged_decode(s, a, st) : sd::launch_paged_chunk(s, a, st));
 }
 
