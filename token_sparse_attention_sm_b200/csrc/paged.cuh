@@ -28,7 +28,7 @@ struct PgSeq {
 // The schedule in the workspace: header, then PgSeq[B + 1] (the last one
 // holds the totals).
 struct PgHead {
-  uint32_t next;  // claim counter of the work items
+  uint32_t next;  // claim counter of the work items after each worker's first
   uint32_t pad[15];
 };
 

@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
                           ch_wait(&sm->item_full[it & 1], (it >> 1) & 1, sm, a.status)))
             break;
         } else {
-          uint32_t x = 0;
-          if (lane == 0) x = atomicAdd(&a.head->next, 1u);
+          uint32_t x = blockIdx.x;
+          if (lane == 0 && it > 0) x = atomicAdd(&a.head->next, 1u);
           x = __shfl_sync(0xffffffffu, x, 0);
           if (!__all_sync(0xffffffffu,
                           ch_wait(&sm->item_empty[it & 1], ((it >> 1) & 1) ^ 1, sm, a.status)))

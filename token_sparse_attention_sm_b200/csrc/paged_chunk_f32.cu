@@ -119,8 +119,9 @@ __global__ void __launch_bounds__(kCfThreads, 1)
   grid_dep_launch();
   const int per_head = a.seqs[a.B].base;
 
-  for (;;) {
-    if (tid == 0) box[0] = (int)min(atomicAdd(&a.head->next, 1u), 0x7fffffffu);
+  for (bool first_item = true;; first_item = false) {
+    if (tid == 0)
+      box[0] = first_item ? (int)blockIdx.x : (int)min(atomicAdd(&a.head->next, 1u), 0x7fffffffu);
     __syncthreads();
     const long long item = box[0];
     __syncthreads();

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_wait();
   grid_dep_launch();
-  if (tid == 0) a.head->next = 0;
+  if (tid == 0) a.head->next = (uint32_t)workers;  // a worker's first item is its own number
   int umax = 1;
   for (int b = lane; b < a.B; b += 32) {
     int u;

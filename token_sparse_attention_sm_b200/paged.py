@@ -266,7 +266,7 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
             return paged_attn(q, K, V, block_table, q_start, kv_lens, window, sinks, max_new, ws,
                               check, return_lse, out, lse)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if lse is None and return_lse:
         lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
     if T == 0:
