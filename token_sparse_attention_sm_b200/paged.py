@@ -42,6 +42,12 @@ class _PagedShape(ctypes.Structure):
                  "max_new")]
 
 
+@functools.lru_cache(maxsize=None)
+def _entry(name: str):
+    """A C entry point of the loaded library."""
+    return getattr(load(), name)
+
+
 @functools.lru_cache(maxsize=512)
 def _shape(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new=0):
     """The C shape of these sizes, by reference (read only by the library)."""
@@ -60,46 +66,46 @@ def _attn_plan(*sizes):
     return sh, int(n.value)
 
 
-def _one_device(*ts) -> int:
+def _one_device(t, *ts) -> int:
     """The index of the device that all given tensors are on."""
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        i = t.get_device()
-        if i != dev:
-            if i < 0:
-                raise ValueError("all tensors must be CUDA tensors")
-            if dev is not None:
-                raise ValueError(f"tensors on cuda:{dev} and on cuda:{i}")
-            dev = i
-    return dev
+    dev = t.get_device()
+    for x in ts:
+        if x is not None and x.get_device() != dev:
+            break
+    else:
+        if dev >= 0:
+            return dev
+    if any(x is not None and not x.is_cuda for x in (t, *ts)):
+        raise ValueError("all tensors must be CUDA tensors")
+    raise ValueError("all tensors must be on one device")
 
 
 def _scratch(ws: Workspace | None, dev: int, nbytes: int, check: bool):
     """The workspace of one call on the current device: the buffer, and the
     current stream."""
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.is_current_stream_capturing():
-        if check:
-            raise ValueError("check=True synchronises: give check=False inside a stream capture")
+    capturing = torch._C._cuda_isCurrentStreamCapturing()
+    if ws is None and not capturing:
+        ws = _stream_ws.get((dev, stream))
         if ws is None:
-            # only the header has to start at zero: the graph clears it
-            buf = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-            if nbytes > _HEADER:
-                buf[:_HEADER].zero_()
-            return None, buf, stream
+            ws = _stream_ws[dev, stream] = Workspace(f"cuda:{dev}")
+        return ws, ws.get(nbytes), stream
+    if capturing and check:
+        raise ValueError("check=True synchronises: give check=False inside a stream capture")
+    if ws is None:
+        # only the header has to start at zero: the graph clears it
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+        if nbytes > _HEADER:
+            buf[:_HEADER].zero_()
+        return None, buf, stream
+    if ws.device.index not in (None, dev):
+        raise ValueError(f"workspace on {ws.device}, tensors on cuda:{dev}")
+    if capturing:
         if ws.buf is None or ws.buf.numel() < nbytes:
             raise ValueError("a workspace cannot grow inside a stream capture: "
                              f"get({nbytes}) before it")
         # the graph keeps this address, also when ws grows later
         ws.kept = getattr(ws, "kept", []) + [ws.buf]
-    elif ws is None:
-        ws = _stream_ws.get((dev, stream))
-        if ws is None:
-            ws = _stream_ws[dev, stream] = Workspace(f"cuda:{dev}")
-    if ws.device.index not in (None, dev):
-        raise ValueError(f"workspace on {ws.device}, tensors on cuda:{dev}")
     return ws, ws.get(nbytes), stream
 
 
@@ -166,16 +172,16 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
     blocks = block_table.shape[1]
     if T < 0:
         raise ValueError("num_tokens must not be negative")
-    for t, s, name in ((new_lens, (B,), "new_lens"), (lens, (B,), "lens"),
-                       (block_table, (B, blocks), "block_table"),
-                       (free_pages, (F,), "free_pages"), (free_count, (1,), "free_count")):
-        _need_int32(t, s, name)
+    _need_int32(new_lens, (B,), "new_lens")
+    _need_int32(lens, (B,), "lens")
+    _need_int32(block_table, (B, blocks), "block_table")
+    _need_int32(free_pages, (F,), "free_pages")
+    _need_int32(free_count, (1,), "free_count")
     sizes = (T, T, B, B + 1, 1)
     res = [positions, slots, kv_lens, q_start, free_left]
-    names = ("positions", "slots", "kv_lens", "q_start", "free_left")
-    for i in range(5):
-        if res[i] is not None:
-            _need_int32(res[i], (sizes[i],), names[i])
+    for t, n, name in zip(res, sizes, ("positions", "slots", "kv_lens", "q_start", "free_left")):
+        if t is not None:
+            _need_int32(t, (n,), name)
     sh = _shape(B, T, 1, 1, 64, _F32, int(page_size), int(num_pages), blocks)
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
@@ -183,14 +189,13 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
                               num_tokens, num_pages, ws, check, kv_lens, q_start, positions, slots,
                               free_left)
     w, buf, stream = _scratch(ws, dev, _HEADER, check)
-    lack = [i for i in range(5) if res[i] is None]
-    if lack:  # one allocation for the results that were not given
-        want = [sizes[i] for i in lack]
-        new = torch.empty(sum(want), dtype=_I32, device=new_lens.device).split(want)
-        for i, v in zip(lack, new):
-            res[i] = v
+    # one allocation for the results that were not given
+    want = [n for t, n in zip(res, sizes) if t is None]
+    if want:
+        new = iter(torch.empty(sum(want), dtype=_I32, device=new_lens.device).split(want))
+        res = [next(new) if t is None else t for t in res]
     positions, slots, kv_lens, q_start, free_left = res
-    _finish(load().sparse_paged_plan(
+    _finish(_entry("sparse_paged_plan")(
         sh, new_lens.data_ptr(), lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), F,
         free_count.data_ptr(), kv_lens.data_ptr(), q_start.data_ptr(), positions.data_ptr(),
         slots.data_ptr(), free_left.data_ptr(), buf.data_ptr(), buf.numel(), stream),
@@ -220,7 +225,7 @@ def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: 
         with torch.cuda.device(dev):
             return paged_append(K, V, k_new, v_new, slots, ws, check)
     w, buf, stream = _scratch(ws, dev, _HEADER, check)
-    _finish(load().sparse_paged_append(
+    _finish(_entry("sparse_paged_append")(
         sh, K.data_ptr(), V.data_ptr(), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
         slots.data_ptr(), buf.data_ptr(), buf.numel(), stream), "paged_append", w, check)
 
@@ -272,7 +277,7 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
     if T == 0:
         return out, lse
     w, buf, stream = _scratch(ws, dev, nbytes, check)
-    _finish(load().sparse_paged_attn(
+    _finish(_entry("sparse_paged_attn")(
         sh, q.data_ptr(), qs, K.data_ptr(), V.data_ptr(), block_table.data_ptr(),
         q_start.data_ptr(), kv_lens.data_ptr(), window, sinks, out.data_ptr(),
         None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), stream),
