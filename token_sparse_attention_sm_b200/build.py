@@ -1,4 +1,5 @@
-"""Build libsparse_decode.so in-tree with nvcc for sm_100a.
+"""Build libsparse_decode.so in-tree with nvcc for sm_100a, and _paged_calls.so,
+the compiled form of the paged calls' Python side, with g++ against torch.
 
 Usage: python -m token_sparse_attention_sm_b200.build [--force]"""
 from __future__ import annotations
@@ -14,6 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsparse_decode.so")
+CALLS = os.path.join(PKG, "_paged_calls.so")
+CALLS_SRC = os.path.join(CSRC, "binding", "paged_calls.cpp")
 OBJDIR = os.path.join(PKG, "_build")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -33,7 +36,33 @@ def _newest_input():
     return max(os.path.getmtime(f) for f in files)
 
 
+def build_calls(force: bool = False) -> str:
+    """_paged_calls.so: torch tensors in, the C entry points (given to it by
+    address) called directly."""
+    newest = max(os.path.getmtime(f) for f in
+                 (CALLS_SRC, os.path.join(INCLUDE, "sparse_decode.h"), os.path.abspath(__file__)))
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+        return CALLS
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    tmp = CALLS + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-DTORCH_EXTENSION_NAME=_paged_calls", *(f"-I{p}" for p in inc), CALLS_SRC,
+        f"-L{os.path.join(root, 'lib')}", "-lc10", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+        "-o", tmp])
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_calls(force)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)

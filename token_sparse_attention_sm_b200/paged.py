@@ -26,6 +26,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
+import os
 
 import torch
 
@@ -64,6 +66,35 @@ def _attn_plan(*sizes):
     sh = _shape(*sizes)
     _check(load().sparse_paged_workspace_size(sh, ctypes.byref(n)), "paged_attn")
     return sh, int(n.value)
+
+
+@functools.lru_cache(maxsize=None)
+def _calls():
+    """The compiled form of the calls (csrc/binding/paged_calls.cpp), given the
+    library's entry points."""
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_paged_calls.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"not built: {path} is missing "
+                           "(run `python -m token_sparse_attention_sm_b200.build`)")
+    spec = importlib.util.spec_from_file_location("_paged_calls", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    lib = load()
+    m.bind(*(ctypes.cast(getattr(lib, f"sparse_paged_{n}"), ctypes.c_void_p).value
+             for n in ("workspace_size", "plan", "append", "attn")))
+    return m
+
+
+def _plain(t):
+    """(compiled calls, workspace, stream) when a call on t's device may take
+    the compiled form: that device is current, nothing is being captured and
+    the stream has a workspace; else None."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device() or torch._C._cuda_isCurrentStreamCapturing():
+        return None
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    ws = _stream_ws.get((dev, stream))
+    return None if ws is None else (_calls(), ws, stream)
 
 
 def _one_device(t, *ts) -> int:
@@ -164,6 +195,18 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
     all int32; kv_lens may be lens and free_left free_count to update them in
     place.  A batch that does not fit raises (SPARSE_ERR_CAPACITY) and takes
     nothing."""
+    if ws is None and q_start is None and positions is None and slots is None:
+        plain = _plain(new_lens)
+        if plain is not None:
+            calls, w, stream = plain
+            r = calls.plan(w.buf, stream, new_lens, lens, block_table, free_pages, free_count,
+                           int(page_size), int(num_tokens), int(num_pages), kv_lens, free_left)
+            if type(r) is tuple:
+                _finish(0, "paged_plan", w, check)
+                return {"kv_lens": r[0], "q_start": r[1], "positions": r[2], "slots": r[3],
+                        "free_left": r[4]}
+            if r is not None:
+                _check(r, "paged_plan")
     dev = _one_device(new_lens, lens, block_table, free_pages, free_count, kv_lens, q_start,
                       positions, slots, free_left)
     if new_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
@@ -209,6 +252,13 @@ def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: 
     wider rows are fine) to their slots [T] int32 of the paged caches K, V
     [num_pages,Hkv,page_size,d]; rows with slot -1 are skipped, and the other
     slots are distinct."""
+    if ws is None:
+        plain = _plain(K)
+        if plain is not None:
+            calls, w, stream = plain
+            r = calls.append(w.buf, stream, K, V, k_new, v_new, slots)
+            if r is not None:
+                return _finish(r, "paged_append", w, check)
     dev = _one_device(K, V, k_new, v_new, slots)
     pages, Hkv, page, d = _cache_dims(K, V)
     if not (k_new.dtype == v_new.dtype == K.dtype):
@@ -244,6 +294,17 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
     (1 for a decode step: the kernels for few rows need it).  Returns
     (out [T,Hq,d], lse [T,Hq] or None); rows behind the last sequence are not
     written."""
+    if ws is None:
+        plain = _plain(q)
+        if plain is not None and (max_new is None or max_new >= 1):
+            calls, w, stream = plain
+            r = calls.attn(w.buf, stream, q, K, V, block_table, q_start, kv_lens, int(window),
+                           int(sinks), int(max_new or 0), return_lse, out, lse)
+            if type(r) is tuple:
+                _finish(0, "paged_attn", w, check)
+                return r
+            if r is not None:
+                _check(r, "paged_attn")
     dev = _one_device(q, K, V, block_table, q_start, kv_lens, out, lse)
     pages, Hkv, page, d = _cache_dims(K, V)
     if q.dim() != 3 or q.dtype != K.dtype:
