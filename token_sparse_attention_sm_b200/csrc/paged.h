@@ -34,8 +34,9 @@ cudaError_t launch_paged_chunk(const PagedShape &s, const PgArgs &a, cudaStream_
 cudaError_t launch_paged_decode_f32(const PagedShape &s, const PgArgs &a, cudaStream_t st);
 cudaError_t launch_paged_chunk_f32(const PagedShape &s, const PgArgs &a, cudaStream_t st);
 // The work items' schedule for row blocks of `tb` tokens, key tiles of `kt`
-// keys and `grid` workers (paged_sched.cu).
+// keys and `grid` workers; what a piece costs besides its tiles, whole or cut, in
+// quarters of a tile (paged_sched.cu).
 cudaError_t launch_paged_schedule(const PagedShape &s, const PgArgs &a, int tb, int kt, int grid,
-                                  cudaStream_t st);
+                                  int whole_cost, int cut_cost, cudaStream_t st);
 
 }  // namespace sd

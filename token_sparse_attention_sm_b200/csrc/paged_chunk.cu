@@ -593,9 +593,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
                                    ((good >> (2 * c)) & 2u ? 0xffff0000u : 0u);
             const uint32_t see = pg_below(hi + 1 - 32 * c) &
                                  (~pg_below(lo - 32 * c) | pg_below(sk - 32 * c)) & pages;
+            // (most blocks of an edge tile are seen whole by all of the warp's rows)
+            if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((see >> i) & 1u)) s[c * 32 + i] = 0xff800000u;
+              for (int i = 0; i < 32; ++i)
+                if (!((see >> i) & 1u)) s[c * 32 + i] = 0xff800000u;
+            }
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i)
@@ -603,11 +606,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (c < 3) ch_wait_ld();
         }
         // the first half's weights do not wait for the maximum: the reference
-        // rarely moves, and if it does they are taken again
-        weights(0, true);
+        // rarely moves, and if it does they are taken again (after the first
+        // tile, which always sets it)
+        if (j > 0) weights(0, true);
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
         const bool raise = mx > m + kChLag || (m == -INFINITY && mx > m);
-        if (__any_sync(0xffffffffu, raise)) {
+        if (j == 0 || __any_sync(0xffffffffu, raise)) {
           const float mn = raise ? mx : m;
           const float corr = raise ? exp2f(m - mn) : 1.f;  // 0 for the first tile
           m = mn;
@@ -735,7 +739,10 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   if (e == cudaSuccess) e = pg_cache_map(&mk, a.K, s, tile);
   if (e == cudaSuccess) e = pg_cache_map(&mv, a.V, s, tile);
   if (e != cudaSuccess) return e;
-  if ((e = launch_paged_schedule(s, a, 2 * TPT, kChKeys, di.sm_count, st)) != cudaSuccess) return e;
+  // starting a piece takes about as long as two tiles, a partial's way out and
+  // back another three
+  if ((e = launch_paged_schedule(s, a, 2 * TPT, kChKeys, di.sm_count, 8, 20, st)) != cudaSuccess)
+    return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attrs[1];
   cfg.stream = st;

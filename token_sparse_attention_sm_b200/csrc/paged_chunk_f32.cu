@@ -319,7 +319,9 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = di.sm_count;  // two CTAs an SM would halve the registers (78 us at d = 64)
-  if ((e = launch_paged_schedule(s, a, kCfRows / s.G(), kCfKeys, grid, st)) != cudaSuccess) return e;
+  // a tile takes 6 (d = 64) or 12 us, starting a piece or merging one a few
+  if ((e = launch_paged_schedule(s, a, kCfRows / s.G(), kCfKeys, grid, 1, 4, st)) != cudaSuccess)
+    return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(kCfThreads, 1, 1);

@@ -176,7 +176,7 @@ cudaError_t launch_paged_plan(const PagedShape &s, const int *new_lens, const in
     e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   // one CTA while its threads take at most four rows each
-  const int cl = s.T <= 4 * kPlThreads && s.B <= 4 * kPlThreads ? 1 : kPlCluster;
+  const int cl = s.T <= kPlRows * kPlThreads ? 1 : kPlCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cl, 1, 1);
   cfg.blockDim = dim3(kPlThreads, 1, 1);

@@ -11,7 +11,7 @@
 // (the longest range cut into 1 .. 192 pieces): pieces per head P =
 // sum nrb * np, waves = ceil(P * Hkv / workers), cost = waves * (longest
 // piece + a fixed part for starting a piece and, when cut, for writing and
-// merging its partial).  The cheapest whose partials fit the workspace wins;
+// merging its partial: the caller's, in quarters of a tile).  The cheapest whose partials fit the workspace wins;
 // ties go to fewer pieces.  One CTA; latency bound (it also resets the call's
 // counters, so nothing of them has to be zero before a call).
 #include "paged.h"
@@ -24,8 +24,6 @@ constexpr int kScThreads = 1024;
 constexpr int kCand = 32;
 __constant__ int kPieces[kCand] = {1,  2,  3,  4,  5,  6,  7,  8,  9,  10, 11,  12,  13,  14,  15,  16,
                                    18, 20, 22, 24, 28, 32, 37, 42, 49, 56, 64, 74, 96, 112, 148, 192};
-// in key tiles: what a piece costs besides its tiles, whole and cut
-constexpr int kPieceCost = 2, kCutCost = 8;
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -52,7 +50,8 @@ __device__ __forceinline__ int sc_blocks(const PgArgs &a, int b, int TB, int KT,
 
 // Every warp walks the batch itself, so the candidates meet at one barrier.
 __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs a, int TB, int KT,
-                                                                    int workers) {
+                                                                    int workers, int whole_cost,
+                                                                    int cut_cost) {
   __shared__ unsigned long long s_cost[kCand];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_wait();
@@ -89,7 +88,7 @@ __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs
       const unsigned long long waves =
           ((unsigned long long)pieces * a.Hkv + workers - 1) / workers;
       s_cost[warp] = slots <= a.slot_cap
-                         ? waves * (unsigned)(longest + (cut ? kCutCost : kPieceCost))
+                         ? waves * (unsigned)(4 * longest + (cut ? cut_cost : whole_cost))
                          : ~0ull;
     }
   }
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs
 }  // namespace
 
 cudaError_t launch_paged_schedule(const PagedShape &, const PgArgs &a, int tb, int kt, int grid,
-                                  cudaStream_t st) {
+                                  int whole_cost, int cut_cost, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1, 1, 1);
   cfg.blockDim = dim3(kScThreads, 1, 1);
@@ -146,7 +145,8 @@ cudaError_t launch_paged_schedule(const PagedShape &, const PgArgs &a, int tb, i
   cfg.attrs = attrs;
   cfg.numAttrs = 0;
   add_pdl_attr(cfg, attrs);
-  return cudaLaunchKernelEx(&cfg, paged_schedule_kernel, a, tb, kt, grid);
+  return cudaLaunchKernelEx(&cfg, paged_schedule_kernel, a, tb, kt, grid, whole_cost,
+                            cut_cost);
 }
 
 }  // namespace sd
