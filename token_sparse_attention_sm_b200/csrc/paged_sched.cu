@@ -57,11 +57,21 @@ __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs
   grid_dep_wait();
   grid_dep_launch();
   if (tid == 0) a.head->next = (uint32_t)workers;  // a worker's first item is its own number
-  int umax = 1;
-  for (int b = lane; b < a.B; b += 32) {
+  // the first 32 sequences' blocks and tiles stay in registers
+  int umax = 1, u0 = 1;
+  const int nrb0 = lane < a.B ? sc_blocks(a, lane, TB, KT, &u0, warp == 0) : 0;
+  if (nrb0) umax = max(umax, u0);
+  for (int b = lane + 32; b < a.B; b += 32) {
     int u;
     if (sc_blocks(a, b, TB, KT, &u, warp == 0)) umax = max(umax, u);
   }
+  auto blocks = [&](int b, int *u) {
+    if (b < 32) {
+      *u = u0;
+      return nrb0;
+    }
+    return sc_blocks(a, b, TB, KT, u, false);
+  };
   umax = __reduce_max_sync(0xffffffffu, umax);
   {
     // this warp's candidate
@@ -70,7 +80,7 @@ __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs
     int longest = 1, cut = 0;
     for (int b = lane; b < a.B; b += 32) {
       int u;
-      const int nrb = sc_blocks(a, b, TB, KT, &u, false);
+      const int nrb = blocks(b, &u);
       if (!nrb) continue;
       const int np = ceil_div(u, C);
       pieces += (long long)nrb * np;
@@ -114,7 +124,7 @@ __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs
     int np = 1, len = 1, items = 0, slots = 0;
     if (b < a.B) {
       int u;
-      const int nrb = sc_blocks(a, b, TB, KT, &u, false);
+      const int nrb = blocks(b, &u);
       np = ceil_div(u, C);
       len = ceil_div(u, np);
       items = nrb * np;
