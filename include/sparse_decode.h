@@ -389,7 +389,9 @@ typedef struct {
 
 /* Bytes of workspace that sparse_paged_attn needs for this shape (the other
  * paged calls need 4096).  A workspace may also serve the entry points above
- * for shapes of B * Hkv <= 256, the calls being ordered.  Synchronous. */
+ * for shapes of B * Hkv <= 256, the calls being ordered.  A call that reports
+ * SPARSE_ERR_TIMEOUT leaves the workspace to be zero-filled again.
+ * Synchronous. */
 sparse_status_t sparse_paged_workspace_size(const sparse_paged_shape_t *shape, size_t *bytes);
 
 /* The block tables and slot map of one batch step, from the requests'

@@ -4,13 +4,15 @@
 // raises m, o and l are scaled by exp2(m_old - m_new)).
 //
 // Both products run on mma.sync m16n8k8 with every fp32 operand split in two
-// tf32 parts, x = hi + lo (hi: the first 11 significant bits, lo: the exact
-// rest, of which the instruction keeps 11 more): a b ~ hi hi + hi lo + lo hi,
-// accumulated in fp32, is off by about 2^-21 |a b|, the error of a handful of
-// fp32 roundings.  Bound by those instructions, three for each product: a
-// 256-token chunk of 8,192 at d = 128, 32 query heads over 8, takes 787 us
-// (43 TFLOP/s; 1,265 with register-tiled multiply-adds), a 250-token chunk of
-// 4,096 at d = 64, 8 over 2, 73 us (96).
+// tf32 parts, x = hi + lo (hi: x rounded to 11 significant bits, lo: the
+// exact rest, of which the instruction keeps 11): a b ~ hi hi + hi lo + lo hi is
+// off by about 2^-22 |a b|.  The instruction's own sums are cut, not rounded, so
+// chains of them are kept short: the mixed products have accumulators of their
+// own, and a tile's share of O starts from zero and is added to O (one chain
+// over all keys was off by 3.9e-6 relative, this 4.2e-7).  Bound by those instructions, three for each product: a
+// 256-token chunk of 8,192 at d = 128, 32 query heads over 8, takes 837 us
+// (40 TFLOP/s; 1,265 with register-tiled multiply-adds), a 250-token chunk of
+// 4,096 at d = 64, 8 over 2, 74 us (96).
 //
 // A worker (CTA) claims items of the schedule: a block of 128 query rows of one
 // (sequence, KV head), 16 per warp, and a piece of its 64-key tiles.  K and V
@@ -48,10 +50,12 @@ __device__ __forceinline__ void cf_ldsm4(const float *p, uint32_t *r) {
                : "r"(smem_u32(p))
                : "memory");
 }
-// x = hi + lo, hi the first 11 significant bits (a mask and a subtraction; the
-// conversion instruction would run on the slow special-function unit)
+// x = hi + lo, hi x rounded to 11 significant bits (halves away from zero).
+// Rounded, not cut: a cut leaves lo with the sign of x, and the lo lo that is
+// dropped then adds up over the sum.  An addition and a
+// mask; the conversion instruction would run on the slow special-function unit.
 __device__ __forceinline__ void cf_split(float x, uint32_t *hi, uint32_t *lo) {
-  *hi = __float_as_uint(x) & 0xffffe000u;
+  *hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   *lo = __float_as_uint(x - __uint_as_float(*hi));
 }
 __device__ __forceinline__ void cf_mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
@@ -61,15 +65,16 @@ __device__ __forceinline__ void cf_mma(float *c, const uint32_t *a, uint32_t b0,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// c += a b, a split already
-__device__ __forceinline__ void cf_mma3(float *c, const uint32_t *ah, const uint32_t *al, float b0,
-                                        float b1) {
+// big + small += a b, a split already: hi hi in big, the two mixed products in
+// small
+__device__ __forceinline__ void cf_mma3(float *big, float *small, const uint32_t *ah,
+                                        const uint32_t *al, float b0, float b1) {
   uint32_t h0, l0, h1, l1;
   cf_split(b0, &h0, &l0);
   cf_split(b1, &h1, &l1);
-  cf_mma(c, ah, l0, l1);
-  cf_mma(c, al, h0, h1);
-  cf_mma(c, ah, h0, h1);
+  cf_mma(small, ah, l0, l1);
+  cf_mma(small, al, h0, h1);
+  cf_mma(big, ah, h0, h1);
 }
 
 // Keys [key0, key0 + 64) of the sequence, those in [0, limit) that any row of
@@ -175,6 +180,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       if (live) {
 #pragma unroll
         for (int i = 0; i < kCfKeys / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        float low4[kCfKeys / 8][4] = {};
         const float *qrow = Qs + (warp * 16 + (lane & 15)) * S + (lane >> 4) * 4;
         const float *krow = Ks + (((lane >> 4) << 3) + (lane & 7)) * S + ((lane >> 3) & 1) * 4;
 #pragma unroll 2
@@ -187,10 +193,15 @@ __global__ void __launch_bounds__(kCfThreads, 1)
           for (int nt = 0; nt < kCfKeys / 16; ++nt) {
             uint32_t kf[4];
             cf_ldsm4(krow + nt * 16 * S + k, kf);
-            cf_mma3(s[2 * nt], ah, al, __uint_as_float(kf[0]), __uint_as_float(kf[1]));
-            cf_mma3(s[2 * nt + 1], ah, al, __uint_as_float(kf[2]), __uint_as_float(kf[3]));
+            cf_mma3(s[2 * nt], low4[2 * nt], ah, al, __uint_as_float(kf[0]), __uint_as_float(kf[1]));
+            cf_mma3(s[2 * nt + 1], low4[2 * nt + 1], ah, al, __uint_as_float(kf[2]),
+                    __uint_as_float(kf[3]));
           }
         }
+#pragma unroll
+        for (int nt = 0; nt < kCfKeys / 8; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] += low4[nt][e];
         const bool whole = key0 + kCfKeys - 1 <= p_first &&
                            (key0 >= low_last || key0 + kCfKeys <= a.sinks) &&
                            *(volatile int *)(box + 1) == 0;
@@ -246,22 +257,30 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         // keys 8 kt + 2 t4, + 1; columns 32 cb + 4 g8 + j are column g8 of the
         // instruction for accumulator 4 cb + j
         const float *vrow = Vs + t4 * 2 * S + g8 * 4;
+        uint32_t ah[kCfKeys / 8][4], al[kCfKeys / 8][4];
 #pragma unroll
         for (int kt = 0; kt < kCfKeys / 8; ++kt) {
-          uint32_t ah[4], al[4];
-          cf_split(s[kt][0], &ah[0], &al[0]);
-          cf_split(s[kt][2], &ah[1], &al[1]);
-          cf_split(s[kt][1], &ah[2], &al[2]);
-          cf_split(s[kt][3], &ah[3], &al[3]);
+          cf_split(s[kt][0], &ah[kt][0], &al[kt][0]);
+          cf_split(s[kt][2], &ah[kt][1], &al[kt][1]);
+          cf_split(s[kt][1], &ah[kt][2], &al[kt][2]);
+          cf_split(s[kt][3], &ah[kt][3], &al[kt][3]);
+        }
 #pragma unroll
-          for (int cb = 0; cb < D / 32; ++cb) {
+        for (int cb = 0; cb < D / 32; ++cb) {
+          float big[4][4] = {}, small[4][4] = {};
+#pragma unroll
+          for (int kt = 0; kt < kCfKeys / 8; ++kt) {
             const float4 v0 = *reinterpret_cast<const float4 *>(vrow + kt * 8 * S + cb * 32);
             const float4 v1 = *reinterpret_cast<const float4 *>(vrow + (kt * 8 + 1) * S + cb * 32);
-            cf_mma3(o[cb * 4], ah, al, v0.x, v1.x);
-            cf_mma3(o[cb * 4 + 1], ah, al, v0.y, v1.y);
-            cf_mma3(o[cb * 4 + 2], ah, al, v0.z, v1.z);
-            cf_mma3(o[cb * 4 + 3], ah, al, v0.w, v1.w);
+            cf_mma3(big[0], small[0], ah[kt], al[kt], v0.x, v1.x);
+            cf_mma3(big[1], small[1], ah[kt], al[kt], v0.y, v1.y);
+            cf_mma3(big[2], small[2], ah[kt], al[kt], v0.z, v1.z);
+            cf_mma3(big[3], small[3], ah[kt], al[kt], v0.w, v1.w);
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[cb * 4 + j][e] += big[j][e] + small[j][e];
         }
       }
       __syncthreads();  // V is used up

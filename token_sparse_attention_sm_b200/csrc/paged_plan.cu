@@ -175,8 +175,11 @@ cudaError_t launch_paged_plan(const PagedShape &s, const int *new_lens, const in
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
+  DeviceInfo di;
+  if ((e = device_info(&di)) != cudaSuccess) return e;
   // one CTA while its threads take at most four rows each
-  const int cl = s.T <= kPlRows * kPlThreads ? 1 : kPlCluster;
+  const int most = di.select_cluster >= kPlCluster ? kPlCluster : 8;
+  const int cl = s.T <= kPlRows * kPlThreads ? 1 : most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cl, 1, 1);
   cfg.blockDim = dim3(kPlThreads, 1, 1);
