@@ -11,31 +11,28 @@
 // Roles (384 threads):
 //  * two TMA warps, one of which claims the items and copies Q, stream K and V
 //    tiles through one ring (one copy per page and tile, 128-byte swizzle);
-//  * a warp per row tile issues its MMAs: S_t = Q_t K^T (M = N = 128) and
+//  * a warp per row tile issues its MMAs: S_t = Q_t K^T (M = 128, N = 64) and
 //    O_t += P_t V, P_t read from tensor memory;
 //  * four softmax warps per row tile, one row per thread: S from tensor
 //    memory, the row's maximum, P = exp2(S scale - m) rounded to bf16 over the
-//    dead S, in two halves so that the product starts on the first, and O
-//    scaled when the maximum moves.
-// A row tile is one chain, scores - softmax - product - scores; the two tiles'
-// chains run side by side, and each has its own issuing warp so that neither
-// waits behind the other's waits.  Tensor memory: S_0, S_1, O_0, O_1 (512
-// columns at d = 128).  (Two 64-key S buffers per row tile took the turn-round
-// out of the chain but cost more: M = 128, N = 64 reads as much of Q for half
-// the work, 725 against 904 TFLOP/s on a 2,048-token chunk of 32K.)
+//    dead S, and O scaled when the maximum moves.
+// K and V tiles have 128 keys, S tiles 64: a row tile has two S buffers, so the
+// scores of the next keys are made while the softmax of these is at work, and
+// each row tile has its own issuing warp, so that neither waits behind the
+// other's waits.  Tensor memory: two S buffers and O per row tile (512 columns
+// at d = 128).  M = 128, N = 64 reads 6 KB of shared memory for 32 cycles of
+// products, 48 cycles; S tiles of 128 keys, one buffer each, need 64 for 64 but
+// make every row tile one chain, scores - softmax - product - scores: 888 TFLOP/s
+// against 1,107 (a 2,048-token chunk of 32K, 32 query heads over 8, d = 128).
+// Handing P over in two halves costs more in the softmax than the earlier
+// product gains (921).
 //
 // The reference m of a row is only raised when the running maximum has left it
 // by more than 2^8: weights then reach 256 instead of 1, the sums stay fp32,
 // the division at the end cancels m, and O is almost never rescaled.
-// P is rounded to bf16 (at most 2^-8 of a weight, independent errors that the
-// sum over keys averages; the result is rounded to bf16 anyway); its sum is
-// taken before the rounding.
-//
-// A step of 128 keys takes about 4,100 cycles for two row tiles, of which the
-// MMAs need 2,000 and the exponentials 2,048: the chains' latencies are the
-// limit, 895-908 TFLOP/s on full blocks (d = 128).  Taking a quarter of the
-// exponentials on the FMA pipe, sixteen softmax warps with half a row each, or
-// interleaving the softmax by 32 keys all came out slower (887, 889, 886).
+// P is rounded to bf16 (2^-9 of each weight on average, independent errors
+// that the sum over keys averages; the result is rounded to bf16 anyway); its
+// sum is taken before the rounding.
 //
 // Every wait is bounded; when one runs out the kernel raises TIMEOUT, all
 // roles leave their loops, the tensor memory is freed and the kernel returns.
@@ -46,7 +43,8 @@
 namespace sd {
 namespace {
 
-constexpr int kChKeys = 128;
+constexpr int kChKeys = 128;  // keys of a K or V tile
+constexpr int kChHalf = 64;   // keys of an S tile
 constexpr int kChSoftWarps = 8;
 constexpr int kChThreads = 384;  // three warpgroups: two of softmax warps; MMA and copies
 // registers a thread: 168 at launch, moved from the third warpgroup to the
@@ -63,21 +61,14 @@ struct ChCfg {
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kQOff = 0, kRingOff = 2 * kQTile;
   static constexpr int kSmallOff = kRingOff + kSlots * kTile;
-  static constexpr int kShareOff = kSmallOff + 1024;  // (max, sum) of 128 rows
-  static constexpr int kSmem = kShareOff + 1024 + 1024;  // + alignment slack
-  static_assert(kSmem <= 227 * 1024, "fits an SM");
+  static constexpr int kSmem = kSmallOff + 1024 + 1024;  // small area, alignment slack
 };
-
-// A block of one row tile only has its key tiles shared out between the two
-// chains (even and odd ones, both with the first row tile's queries) if there
-// are this many, and their results joined at the end.
-constexpr int kChAlternate = 4;
 
 // One work item, as the TMA warp found it.
 struct ChItem {
   int b, h, row0, t0, rows;            // rows: query rows of the block
   int p_first, p_last, low;            // positions of its first and last token; lowest key of a window
-  int u0, u1;                          // the piece's tiles
+  int u0, u1, halves;                  // the piece's tiles, and the 64-key halves to run
   int sink_tiles, lo;
   int np, piece, first;                // partial slots: (first + piece) * Hkv + h
   int valid;                           // 0: no more items
@@ -86,7 +77,10 @@ struct ChItem {
 struct ChSmall {
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_ready[2][2], pv_done[2], o_empty[2], wg[2], pair;  // p_ready: half a tile each
+  // [row tile][S buffer]: a buffer's phases alternate strictly, so a parity
+  // wait is never two phases off
+  uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];
+  uint64_t o_empty[2], wg[2];
   uint64_t item_full[2], item_empty[2];
   ChItem item[2];
   uint32_t ok[8];
@@ -164,17 +158,6 @@ __device__ __forceinline__ void ch_tma(uint32_t dst, const CUtensorMap *map, int
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ uint4 lds128_at(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t ch_join(uint32_t x, float fx, uint32_t y, float fy) {
-  return __float_as_uint(__uint_as_float(x) * fx + __uint_as_float(y) * fy);
-}
 // one lane of a converged warp, always the same
 __device__ __forceinline__ bool ch_elect() {
   uint32_t p;
@@ -209,8 +192,7 @@ __device__ __forceinline__ bool ch_wait(uint64_t *bar, uint32_t parity, ChSmall 
   return true;
 }
 
-// ALT: blocks of one row tile use both chains
-template <int D, bool ALT>
+template <int D>
 __global__ void __launch_bounds__(kChThreads, 1)
     paged_chunk_kernel(const PgArgs a, const __grid_constant__ CUtensorMap mapQ,
                        const __grid_constant__ CUtensorMap mapK,
@@ -238,12 +220,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
     }
     mbar_init(&sm->q_full, 1);
     mbar_init(&sm->q_empty, 2);
-    mbar_init(&sm->pair, kChSoftWarps);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sm->s_full[t], 1);
-      mbar_init(&sm->p_ready[t][0], 4);
-      mbar_init(&sm->p_ready[t][1], 4);
-      mbar_init(&sm->pv_done[t], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sm->s_full[t][i], 1);
+        mbar_init(&sm->p_ready[t][i], 4);
+        mbar_init(&sm->pv_done[t][i], 1);
+      }
       mbar_init(&sm->o_empty[t], 4);
       mbar_init(&sm->wg[t], 4);
       mbar_init(&sm->item_full[t], 1);
@@ -312,6 +294,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
               I.lo = t.lo;
               I.u0 = min(piece * sq.len, t.units());
               I.u1 = min(t.units(), I.u0 + sq.len);
+              // no row sees the second half of a tile that ends a range early
+              I.halves = 2 * (I.u1 - I.u0);
+              if (I.u1 > I.u0 && I.u1 == t.units() &&
+                  t.tile(I.u1 - 1) * kChKeys + kChHalf > p_last)
+                --I.halves;
               I.np = sq.np;
               I.piece = piece;
               I.first = sq.slot + rb * sq.np;
@@ -415,120 +402,99 @@ __global__ void __launch_bounds__(kChThreads, 1)
       // live in uniform registers: issued from a divergent lane 0, with each
       // descriptor moved over on its own, an instruction took about 100 cycles.)
       const int t = warp - kChMmaWarp;
-      constexpr uint32_t idS = ch_idesc(kChKeys, false), idPV = ch_idesc(D, true);
+      constexpr uint32_t idS = ch_idesc(kChHalf, false), idPV = ch_idesc(D, true);
       const bool lead = ch_elect();
       const uint32_t tS = ch_uniform(tmem + t * 128), tO = ch_uniform(tmem + 256 + t * 128);
-      const uint64_t q_own = ch_desc(ch_uniform(base + C::kQOff + t * C::kQTile), 16, 1024);
-      const uint64_t q_first = ch_desc(ch_uniform(base + C::kQOff), 16, 1024);
+      const uint64_t q = ch_desc(ch_uniform(base + C::kQOff + t * C::kQTile), 16, 1024);
       const uint32_t ring = ch_uniform(base + C::kRingOff);
-      const uint32_t kcol = tl.col / 16, vstep = 2 * tl.group / 16;  // 16-byte units
+      // in 16-byte units: between column blocks, 16 and 64 keys
+      const uint32_t kcol = tl.col / 16, vstep = 2 * tl.group / 16, half = 8 * tl.group / 16;
       int slot = 0;  // ring position of the next tile
-      uint32_t phase = 0, q_count = 0, pv_cnt = 0, o_cnt = 0;
+      uint32_t phase = 0, q_count = 0, o_cnt = 0;
+      uint32_t s_cnt = 0, p_cnt = 0;  // halves whose scores, whose product were issued
       auto step = [&]() {
         if (++slot == C::kSlots) slot = 0, phase ^= 1u;
       };
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         return __all_sync(0xffffffffu, ch_wait(bar, parity & 1u, sm, a.status)) != 0;
       };
-      // S of the K tile in the ring's next slot, which it frees
-      auto scores = [&](uint64_t q, bool last) {
-        const uint64_t k = ch_desc(ch_uniform(ring + slot * C::kTile), 16, tl.group);
-        if (lead) {
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            ch_mma_ss(tS, q + ((s >> 2) * (128 * 128) + (s & 3) * 32) / 16,
-                      k + (s >> 2) * kcol + (s & 3) * 2, idS, s > 0);
-          ch_commit(&sm->s_full[t]);
-          ch_commit(&sm->empty[slot]);
-          if (last) ch_commit(&sm->q_empty);
-        }
-        __syncwarp();
-        step();
-      };
       bool ok = true;
       for (int it = 0; ok; ++it) {
         if (!(ok = wait(&sm->item_full[it & 1], it >> 1))) break;
         const ChItem &I = sm->item[it & 1];
-        const int valid = ch_uniform(I.valid), n = ch_uniform(I.u1 - I.u0);
-        const bool two = ch_uniform(I.rows) > TPT * G;  // row tiles
+        const int valid = ch_uniform(I.valid), n = ch_uniform(I.halves);
+        const bool mine = t == 0 || ch_uniform(I.rows) > TPT * G;
         __syncwarp();
         if (lead) mbar_arrive(&sm->item_empty[it & 1]);
         if (!valid) break;
         if (n <= 0) continue;
-        const bool alt = ALT && !two && n >= kChAlternate;
         if (!(ok = wait(&sm->q_full, q_count++))) break;
-        // a ring slot that only the other row tile's chain uses
-        auto skip = [&]() {
-          ok = wait(&sm->full[slot], phase);
-          if (lead) mbar_arrive(&sm->empty[slot]);
-          __syncwarp();
-          step();
-        };
-        if (t == 1 && !two && !alt) {
-          for (int j = 0; j < 2 * n && ok; ++j) skip();
+        if (!mine) {  // no rows in this tile: free what the other one uses
+          for (int j = 0; j < (n + 1) / 2 * 2 && ok; ++j) {
+            ok = wait(&sm->full[slot], phase);
+            if (lead) mbar_arrive(&sm->empty[slot]);
+            step();
+          }
           if (lead) mbar_arrive(&sm->q_empty);
           __syncwarp();
           continue;
         }
-        // turns: this chain has every other key tile, from its own number on
-        auto chain = [&](auto turns) {
-          constexpr bool kTurns = decltype(turns)::value;
-          const uint64_t q = kTurns ? q_first : q_own;
-          if (kTurns && t == 1) {
-            skip();
-            if (ok) skip();
-            if (!ok) return;
-          }
-          // (the last P of the item before was used up: its end was waited for)
-          if (!(ok = wait(&sm->full[slot], phase))) return;
-          ch_fence_after();
-          // (in turns, the queries' space is freed by the first chain's scores and,
-          // once it has served to join the results, by the softmax)
-          const bool frees_q = !(kTurns && t == 1);
-          scores(q, frees_q && (kTurns ? n <= 2 : n == 1));
-          for (int j = kTurns ? t : 0; j < n; j += kTurns ? 2 : 1) {
+        int kslot = 0, vslot = 0;
+        // scores of half i into the buffer whose turn it is; the last half of a
+        // K tile frees it
+        auto scores = [&](int i) {
+          if ((i & 1) == 0) {
+            kslot = slot;
             if (!(ok = wait(&sm->full[slot], phase))) return;
-            if (j == (kTurns ? t : 0) && o_cnt++ > 0)  // O of the item before was read
-              if (!(ok = wait(&sm->o_empty[t], o_cnt - 2))) return;
-            const uint64_t v = ch_desc(ch_uniform(ring + slot * C::kTile), tl.col, tl.group);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!(ok = wait(&sm->p_ready[t][h], pv_cnt))) return;
-              ch_fence_after();
-              if (lead) {
-#pragma unroll
-                for (int kk = h * 4; kk < h * 4 + 4; ++kk)
-                  ch_mma_ts(tO, tS + kk * 8, v + kk * vstep, idPV,
-                            kk > 0 ? 1u : (uint32_t)(j > (kTurns ? t : 0)));
-              }
-              __syncwarp();
-            }
-            if (lead) {
-              ch_commit(&sm->pv_done[t]);
-              ch_commit(&sm->empty[slot]);
-            }
-            __syncwarp();
             step();
-            if (kTurns && j + 1 < n) {
-              skip();
-              if (ok) skip();
-              if (!ok) return;
-            }
-            const int next = j + (kTurns ? 2 : 1);
-            if (next < n && !(ok = wait(&sm->full[slot], phase))) return;
-            // S overwrites the P that the product just issued reads
-            if (!(ok = wait(&sm->pv_done[t], pv_cnt++))) return;
-            if (next < n) {
-              ch_fence_after();
-              scores(q, frees_q && next + (kTurns ? 2 : 1) >= n);
-            }
           }
+          const uint32_t buf = s_cnt & 1;
+          // the P that the buffer held is used up
+          if (s_cnt >= 2 && !(ok = wait(&sm->pv_done[t][buf], (s_cnt >> 1) - 1))) return;
+          ch_fence_after();
+          const uint64_t k =
+              ch_desc(ch_uniform(ring + kslot * C::kTile), 16, tl.group) + (i & 1) * half;
+          if (lead) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              ch_mma_ss(tS + buf * 64, q + ((s >> 2) * (128 * 128) + (s & 3) * 32) / 16,
+                        k + (s >> 2) * kcol + (s & 3) * 2, idS, s > 0);
+            ch_commit(&sm->s_full[t][buf]);
+            if ((i & 1) || i == n - 1) ch_commit(&sm->empty[kslot]);
+            if (i == n - 1) ch_commit(&sm->q_empty);
+          }
+          __syncwarp();
+          ++s_cnt;
         };
-        if constexpr (ALT) {
-          if (alt) chain(std::true_type{});
-          else chain(std::false_type{});
-        } else {
-          chain(std::false_type{});
+        scores(0);
+        for (int i = 0; i < n && ok; ++i) {
+          if ((i & 1) == 0) {  // V follows its K in the ring
+            vslot = slot;
+            if (!(ok = wait(&sm->full[slot], phase))) break;
+            step();
+          }
+          // the next scores run while the softmax of these is at work
+          if (i + 1 < n) {
+            scores(i + 1);
+            if (!ok) break;
+          }
+          const uint32_t buf = p_cnt & 1;
+          if (i == 0 && o_cnt++ > 0)  // O of the item before has been read
+            if (!(ok = wait(&sm->o_empty[t], o_cnt - 2))) break;
+          if (!(ok = wait(&sm->p_ready[t][buf], p_cnt >> 1))) break;
+          ch_fence_after();
+          const uint64_t v =
+              ch_desc(ch_uniform(ring + vslot * C::kTile), tl.col, tl.group) + (i & 1) * half;
+          if (lead) {
+#pragma unroll
+            for (int kk = 0; kk < kChHalf / 16; ++kk)
+              ch_mma_ts(tO, tS + buf * 64 + kk * 8, v + kk * vstep, idPV,
+                        kk > 0 ? 1u : (uint32_t)(i > 0));
+            ch_commit(&sm->pv_done[t][buf]);
+            if ((i & 1) || i == n - 1) ch_commit(&sm->empty[vslot]);
+          }
+          __syncwarp();
+          ++p_cnt;
         }
       }
     }
@@ -544,20 +510,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
     uint32_t phase = 0, s_cnt = 0, wg_cnt = 0;
     int unit = 0;
     bool ok = true;
-    constexpr uint32_t all_ok = (1u << (kChKeys / 16)) - 1u;
+    constexpr uint32_t all_ok = (1u << (kChHalf / 16)) - 1u;
     auto step = [&]() {
       if (++ring == C::kSlots) ring = 0, phase ^= 1u;
-    };
-    // (max, sum) of a row from the other chain; the space of the second row
-    // tile's queries, for its O
-    float2 *share = reinterpret_cast<float2 *>(raw + (base - raw_s) + C::kShareOff);
-    uint32_t pair_cnt = 0;
-    auto pair_sync = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->pair);
-      const bool w = ch_wait(&sm->pair, pair_cnt & 1, sm, a.status);
-      ++pair_cnt;
-      return __all_sync(0xffffffffu, w) != 0;
     };
     // the four warps of the tile meet (bounded)
     auto wg_sync = [&]() {
@@ -575,124 +530,105 @@ __global__ void __launch_bounds__(kChThreads, 1)
         if (lane == 0) mbar_arrive(&sm->item_empty[it & 1]);
       };
       if (!I.valid) break;
-      const int n = max(0, I.u1 - I.u0), tile_rows = TPT * G;
-      const bool alt = ALT && I.rows <= tile_rows && n >= kChAlternate;
-      if (t == 1 && I.rows <= tile_rows && !alt) {  // nothing here: keep count of the ring
-        for (int j = 0; j < n; ++j) step(), step();
-        unit += n;
+      const int n = max(0, I.halves), tile_rows = TPT * G;
+      if (t == 1 && I.rows <= tile_rows) {  // no second row tile: keep count of the ring
+        for (int j = 0; j < n; j += 2) {
+          step(), step();
+          ++unit;
+        }
         done();
         continue;
       }
-      const int rt = alt ? 0 : t;           // row tile
-      const int br = rt * tile_rows + r;  // row of the block
+      const int br = t * tile_rows + r;  // row of the block
       const bool live = r < tile_rows && br < I.rows;
       const int pos = live ? I.p_first + a.by_G(br) : -1;
       const int low = pg_window_low(pos, a.window);
-      const int pf = I.p_first + rt * TPT, pl = min(I.p_last, pf + TPT - 1);  // the tile's tokens
+      const int pf = I.p_first + t * TPT, pl = min(I.p_last, pf + TPT - 1);  // the tile's tokens
       const int low_last = pg_window_low(pl, a.window);
       float m = -INFINITY, l = 0.f;
-      bool begun = false;  // a tile of this item has been through this chain
+      int vslot = 0;
+      uint32_t good8 = 0;
       for (int j = 0; j < n; ++j) {
-        if (alt && (j & 1) != t) {
-          step(), step();
-          ++unit;
-          continue;
+        const int u = I.u0 + (j >> 1), h = j & 1;
+        const int key0 = (u < I.sink_tiles ? u : u - I.sink_tiles + I.lo) * kChKeys + h * kChHalf;
+        const uint32_t buf = s_cnt & 1, tB = tS + buf * 64;
+        ok = ch_wait(&sm->s_full[t][buf], (s_cnt >> 1) & 1, sm, a.status);
+        ch_fence_after();
+        uint32_t s[kChHalf], p[32];
+        ch_ld32(tB, s);
+        ch_ld32(tB + 32, s + 32);
+        if (h == 0) {
+          step();
+          vslot = ring;
+          // also orders this after the V warp's note on the tile's pages
+          if (ok) ok = ch_wait(&sm->full[vslot], phase, sm, a.status);
+          step();
+          good8 = sm->ok[unit++ & 7];
         }
-        const int u = I.u0 + j;
-        const int key0 = (u < I.sink_tiles ? u : u - I.sink_tiles + I.lo) * kChKeys;
-        step();
-        const int vslot = ring;
-        const uint32_t vphase = phase;
-        step();
-        ok = ch_wait(&sm->s_full[t], s_cnt & 1, sm, a.status);
-        ++s_cnt;
-        // also orders this after the TMA warp's note on the tile's pages
-        if (ok) ok = ch_wait(&sm->full[vslot], vphase, sm, a.status);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
-        ch_fence_after();
-        const uint32_t good = sm->ok[unit & 7];
-        ++unit;
-        if (key0 + kChKeys > I.p_last + 1 || (key0 < I.low && key0 + kChKeys > a.sinks)) {
+        const uint32_t good = (good8 >> (4 * h)) & all_ok;
+        if (key0 + kChHalf > I.p_last + 1 || (key0 < I.low && key0 + kChHalf > a.sinks)) {
           // V rows that no row of the block sees may hold anything: clear them
           // (each tile's warps before its own product; both write zeros)
-          const int key = key0 + r;
+          const int key = key0 + (r >> 1);
           if (key > I.p_last || (key < I.low && key >= a.sinks)) {
+            const int vr = h * kChHalf + (r >> 1);
             const uint32_t v =
-                base + C::kRingOff + vslot * C::kTile + (r >> 3) * tl.group + (r & 7) * 128;
+                base + C::kRingOff + vslot * C::kTile + (vr >> 3) * tl.group + (vr & 7) * 128;
 #pragma unroll
-            for (int c = 0; c < C::CB; ++c)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                 v + c * tl.col + ((i + r) & 7) * 16),
-                             "r"(0u)
-                             : "memory");
+            for (int i = 0; i < D / 16; ++i) {  // 16-byte pieces, half a row
+              const int c = (r & 1) * (D / 16) + ((i + (r >> 1)) & (D / 16 - 1));
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                               v + (c >> 3) * tl.col + (c & 7) * 16),
+                           "r"(0u)
+                           : "memory");
+            }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        const bool whole = key0 + kChKeys - 1 <= pf &&
-                           (key0 >= low_last || key0 + kChKeys <= a.sinks) && good == all_ok;
-        uint32_t s[128], p[32];
-        uint64_t sum2[2];
-        const uint64_t scale2 = pg_f2(a.scale_log2, a.scale_log2);
-        // weights of keys 64 c .. 64 c + 63 against the reference m
-        auto weights = [&](int c, bool fresh) {
-          const float use = m == -INFINITY ? 0.f : m;
-          const uint64_t neg2 = pg_f2(-use, -use);
-          if (fresh) sum2[0] = sum2[1] = 0ull;  // pairs of zeros
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int k = c * 64 + i * 2;
-            float p0, p1;
-            pg_split(pg_fma2(pg_u2(s[k], s[k + 1]), scale2, neg2), &p0, &p1);
-            p0 = pg_exp2(p0);
-            p1 = pg_exp2(p1);
-            sum2[i & 1] = pg_add2(sum2[i & 1], pg_f2(p0, p1));
-            p[i] = ch_pack(p0, p1);
-          }
-        };
-        // four accumulators, each block's maximum while the next one is read
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        ch_ld32(tS, s);
+        const bool whole = key0 + kChHalf - 1 <= pf &&
+                           (key0 >= low_last || key0 + kChHalf <= a.sinks) && good == all_ok;
         ch_wait_ld();
+        if (!whole) {
+          // the row's keys, a bit each
+          const int hi = pos - key0, lo = low - key0, sk = a.sinks - key0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < 3) ch_ld32(tS + (c + 1) * 32, s + (c + 1) * 32);
-          if (!whole) {
-            // the row's keys of the block, a bit each
-            const int hi = pos - key0, lo = low - key0, sk = a.sinks - key0;
-            const uint32_t pages = ((good >> (2 * c)) & 1u ? 0xffffu : 0u) |
-                                   ((good >> (2 * c)) & 2u ? 0xffff0000u : 0u);
-            const uint32_t see = pg_below(hi + 1 - 32 * c) &
-                                 (~pg_below(lo - 32 * c) | pg_below(sk - 32 * c)) & pages;
+          for (int w = 0; w < 2; ++w) {
+            const uint32_t pages = ((good >> (2 * w)) & 1u ? 0xffffu : 0u) |
+                                   ((good >> (2 * w)) & 2u ? 0xffff0000u : 0u);
+            const uint32_t see = pg_below(hi + 1 - 32 * w) &
+                                 (~pg_below(lo - 32 * w) | pg_below(sk - 32 * w)) & pages;
             // (most blocks of an edge tile are seen whole by all of the warp's rows)
             if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (!((see >> i) & 1u)) s[c * 32 + i] = 0xff800000u;
+                if (!((see >> i) & 1u)) s[w * 32 + i] = 0xff800000u;
             }
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(s[c * 32 + i]));
-          if (c < 3) ch_wait_ld();
         }
-        // the first half's weights do not wait for the maximum: the reference
-        // rarely moves, and if it does they are taken again (after the first
-        // tile, which always sets it)
-        if (begun) weights(0, true);
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kChHalf; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(s[i]));
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
         const bool raise = mx > m + kChLag || (m == -INFINITY && mx > m);
-        if (!begun || __any_sync(0xffffffffu, raise)) {
+        if (__any_sync(0xffffffffu, raise)) {
           const float mn = raise ? mx : m;
-          const float corr = raise ? exp2f(m - mn) : 1.f;  // 0 for the first tile
+          const float corr = raise ? exp2f(m - mn) : 1.f;  // 0 for the first half
           m = mn;
           l *= corr;
-          if (begun) {
-            // the product before has finished: S of this tile came after it
+          if (j > 0) {
+            // the product before this one has to finish (the one before that
+            // did before this buffer's scores were issued)
+            const uint32_t before = s_cnt - 1;
+            ok = ch_wait(&sm->pv_done[t][before & 1], (before >> 1) & 1, sm, a.status);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            ch_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               ch_ld32(tO + c * 32, p);
@@ -702,73 +638,39 @@ __global__ void __launch_bounds__(kChThreads, 1)
               ch_st32(tO + c * 32, p);
             }
           }
-          weights(0, true);
         }
+        const float use = m == -INFINITY ? 0.f : m;
+        const uint64_t scale2 = pg_f2(a.scale_log2, a.scale_log2), neg2 = pg_f2(-use, -use);
+        uint64_t sum2[2] = {0ull, 0ull};  // pairs of zeros
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c == 1) weights(1, false);
-          ch_st32(tS + c * 32, p);
-          ch_wait_st();
-          ch_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->p_ready[t][c]);
+        for (int i = 0; i < 32; ++i) {
+          float p0, p1;
+          pg_split(pg_fma2(pg_u2(s[2 * i], s[2 * i + 1]), scale2, neg2), &p0, &p1);
+          p0 = pg_exp2(p0);
+          p1 = pg_exp2(p1);
+          sum2[i & 1] = pg_add2(sum2[i & 1], pg_f2(p0, p1));
+          p[i] = ch_pack(p0, p1);
         }
-        begun = true;
+        ch_st32(tB, p);
         float a0, a1;
         pg_split(pg_add2(sum2[0], sum2[1]), &a0, &a1);
         l += a0 + a1;
+        ch_wait_st();
+        ch_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->p_ready[t][buf]);
+        ++s_cnt;
       }
       if (!ok) break;
       // ---- the piece's result ----------------------------------------------------------
       if (n > 0) {
         // every product of the item is done when its last one is
-        ok = ch_wait(&sm->pv_done[t], (s_cnt - 1) & 1, sm, a.status);
+        const uint32_t last = s_cnt - 1;
+        ok = ch_wait(&sm->pv_done[t][last & 1], (last >> 1) & 1, sm, a.status);
         if (!__all_sync(0xffffffffu, ok)) break;
         ch_fence_after();
       }
-      // In turns: the second chain hands its O over in two halves of the columns,
-      // through the space of the second row tile's queries.
-      float own = 1.f, other = 0.f;  // factors of the two chains' O
-      const uint32_t xrow = base + C::kQOff + C::kQTile + r * (D * 2);
-      auto xaddr = [&](int i) { return xrow + ((i + r) & (D / 8 - 1)) * 16; };  // 16-byte pieces
-      if (alt && t == 1) {
-        share[r] = make_float2(m, l);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half == 1 && !(ok = pair_sync())) break;  // the first half has been read
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            uint32_t o[32];
-            ch_ld32(tO + half * (D / 2) + c * 32, o);
-            ch_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(xaddr(c * 8 + i)),
-                           "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
-                           : "memory");
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (!(ok = pair_sync())) break;  // this half is there
-        }
-        if (!ok) break;
-        ch_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->o_empty[t]);
-        if (!(ok = pair_sync())) break;  // both have been read
-        done();
-        continue;
-      }
-      if (alt) {
-        if (!(ok = pair_sync())) break;  // the other's first half is there
-        const float2 e = share[r];
-        const float top = fmaxf(m, e.x), use = top == -INFINITY ? 0.f : top;
-        own = exp2f(m - use);
-        other = exp2f(e.x - use);
-        m = top;
-        l = l * own + e.y * other;
-      }
-      const size_t at =
-          (size_t)(I.row0 + I.t0 + a.by_G(br)) * a.Hq + I.h * G + br - a.by_G(br) * G;
+      const size_t at = (size_t)(I.row0 + I.t0 + a.by_G(br)) * a.Hq + I.h * G + br - a.by_G(br) * G;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const size_t per = (size_t)a.part_rows * D;
       const size_t first = (size_t)I.first * a.Hkv + I.h;
@@ -783,19 +685,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
-        }
-        if (alt) {
-          if (c == D / 64) {  // the other's second half
-            if (!(ok = pair_sync()) || !(ok = pair_sync())) break;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 x = lds128_at(xaddr((c & (D / 64 - 1)) * 8 + i));
-            o[4 * i] = ch_join(o[4 * i], own, x.x, other);
-            o[4 * i + 1] = ch_join(o[4 * i + 1], own, x.y, other);
-            o[4 * i + 2] = ch_join(o[4 * i + 2], own, x.z, other);
-            o[4 * i + 3] = ch_join(o[4 * i + 3], own, x.w, other);
-          }
         }
         if (live) {
           if (I.np == 1) {
@@ -816,12 +705,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
                   make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
-      }
-      if (!ok) break;
-      if (alt) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        if (!(ok = pair_sync())) break;  // read: the queries' space is free
-        if (r == 0) mbar_arrive(&sm->q_empty);
       }
       ch_fence_before();
       __syncwarp();
@@ -860,13 +743,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
                  : "memory");
 }
 
-template <int D, bool ALT>
+template <int D>
 cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   using C = ChCfg<D>;
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
-  auto kern = paged_chunk_kernel<D, ALT>;
+  auto kern = paged_chunk_kernel<D>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const PgTile tile = pg_tile(s.page, s.blocks, D * 2, kChKeys);
@@ -896,14 +779,7 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_paged_chunk(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
-  // Blocks of one row tile leave half of the kernel idle unless the two chains
-  // take turns at the key tiles, but the code for that slows full blocks down by
-  // 4 % (2,048-token chunk of 32K: 1,200 against 1,250 us).  So it goes by the
-  // batch's average: with it, one 1,000-token chunk among 31 decoding sequences
-  // takes 207 instead of 215 us, a 646-token one among ten 53 instead of 65.
-  const bool alt = (long long)s.T * s.G() <= 256ll * s.B;
-  if (s.d == 64) return alt ? run<64, true>(s, a, st) : run<64, false>(s, a, st);
-  return alt ? run<128, true>(s, a, st) : run<128, false>(s, a, st);
+  return s.d == 64 ? run<64>(s, a, st) : run<128>(s, a, st);
 }
 
 }  // namespace sd
