@@ -14,8 +14,8 @@
 //  * a warp per row tile issues its MMAs: S_t = Q_t K^T (M = 128, N = 64) and
 //    O_t += P_t V, P_t read from tensor memory;
 //  * four softmax warps per row tile, one row per thread: S from tensor
-//    memory, the row's maximum, P = exp2(S scale - m) rounded to bf16 over the
-//    dead S, and O scaled when the maximum moves.
+//    memory, P = exp2(S scale - m) rounded to bf16 over the dead S, the row's
+//    maximum meanwhile, and O scaled when m has to move.
 // K and V tiles have 128 keys, S tiles 64: a row tile has two S buffers, so the
 // scores of the next keys are made while the softmax of these is at work, and
 // each row tile has its own issuing warp, so that neither waits behind the
@@ -23,7 +23,7 @@
 // at d = 128).  M = 128, N = 64 reads 6 KB of shared memory for 32 cycles of
 // products, 48 cycles; S tiles of 128 keys, one buffer each, need 64 for 64 but
 // make every row tile one chain, scores - softmax - product - scores: 888 TFLOP/s
-// against 1,107 (a 2,048-token chunk of 32K, 32 query heads over 8, d = 128).
+// against 1,107 (1,135 now; a 2,048-token chunk of 32K, 32 query heads over 8, d = 128).
 // Handing P over in two halves costs more in the softmax than the earlier
 // product gains (921).
 //
@@ -103,6 +103,12 @@ __device__ __forceinline__ void ch_st32(uint32_t taddr, const uint32_t *r) {
       : "memory");
 }
 
+// max(a, b, c) of fp32 values
+__device__ __forceinline__ float ch_max3(float a, uint32_t b, uint32_t c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return r;
+}
 __device__ __forceinline__ void ch_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -546,120 +552,143 @@ __global__ void __launch_bounds__(kChThreads, 1)
       const int pf = I.p_first + t * TPT, pl = min(I.p_last, pf + TPT - 1);  // the tile's tokens
       const int low_last = pg_window_low(pl, a.window);
       float m = -INFINITY, l = 0.f;
-      int vslot = 0;
+      const int u0 = I.u0, sink_tiles = I.sink_tiles, hi_first = I.lo - I.sink_tiles;
+      const int last_key = I.p_last, first_low = I.low;
+      int vslot = 0, key0 = 0;
       uint32_t good8 = 0;
-      for (int j = 0; j < n; ++j) {
-        const int u = I.u0 + (j >> 1), h = j & 1;
-        const int key0 = (u < I.sink_tiles ? u : u - I.sink_tiles + I.lo) * kChKeys + h * kChHalf;
-        const uint32_t buf = s_cnt & 1, tB = tS + buf * 64;
-        ok = ch_wait(&sm->s_full[t][buf], (s_cnt >> 1) & 1, sm, a.status);
-        ch_fence_after();
-        uint32_t s[kChHalf], p[32];
-        ch_ld32(tB, s);
-        ch_ld32(tB + 32, s + 32);
-        if (h == 0) {
-          step();
-          vslot = ring;
-          // also orders this after the V warp's note on the tile's pages
-          if (ok) ok = ch_wait(&sm->full[vslot], phase, sm, a.status);
-          step();
-          good8 = sm->ok[unit++ & 7];
-        }
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        const uint32_t good = (good8 >> (4 * h)) & all_ok;
-        if (key0 + kChHalf > I.p_last + 1 || (key0 < I.low && key0 + kChHalf > a.sinks)) {
-          // V rows that no row of the block sees may hold anything: clear them
-          // (each tile's warps before its own product; both write zeros)
-          const int key = key0 + (r >> 1);
-          if (key > I.p_last || (key < I.low && key >= a.sinks)) {
-            const int vr = h * kChHalf + (r >> 1);
-            const uint32_t v =
-                base + C::kRingOff + vslot * C::kTile + (vr >> 3) * tl.group + (vr & 7) * 128;
+      for (int j0 = 0; j0 < n && ok; j0 += 2) {
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {  // 16-byte pieces, half a row
-              const int c = (r & 1) * (D / 16) + ((i + (r >> 1)) & (D / 16 - 1));
-              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                               v + (c >> 3) * tl.col + (c & 7) * 16),
-                           "r"(0u)
-                           : "memory");
+        for (int h = 0; h < 2; ++h) {
+          const int j = j0 + h;
+          if (j >= n) break;
+          if (h == 0) {
+            const int u = u0 + (j0 >> 1);
+            key0 = (u < sink_tiles ? u : u + hi_first) * kChKeys;
+          } else {
+            key0 += kChHalf;
+          }
+          const uint32_t buf = s_cnt & 1, tB = tS + buf * 64;
+          ok = ch_wait(&sm->s_full[t][buf], (s_cnt >> 1) & 1, sm, a.status);
+          ch_fence_after();
+          uint32_t s[kChHalf], p[32];
+          ch_ld32(tB, s);
+          ch_ld32(tB + 32, s + 32);
+          if (h == 0) {
+            step();
+            vslot = ring;
+            // also orders this after the V warp's note on the tile's pages
+            if (ok) ok = ch_wait(&sm->full[vslot], phase, sm, a.status);
+            step();
+            good8 = sm->ok[unit++ & 7];
+          }
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          const uint32_t good = (good8 >> (4 * h)) & all_ok;
+          if (key0 + kChHalf > last_key + 1 || (key0 < first_low && key0 + kChHalf > a.sinks)) {
+            // V rows that no row of the block sees may hold anything: clear them
+            // (each tile's warps before its own product; both write zeros)
+            const int key = key0 + (r >> 1);
+            if (key > last_key || (key < first_low && key >= a.sinks)) {
+              const int vr = h * kChHalf + (r >> 1);
+              const uint32_t v =
+                  base + C::kRingOff + vslot * C::kTile + (vr >> 3) * tl.group + (vr & 7) * 128;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {  // 16-byte pieces, half a row
+                const int c = (r & 1) * (D / 16) + ((i + (r >> 1)) & (D / 16 - 1));
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                 v + (c >> 3) * tl.col + (c & 7) * 16),
+                             "r"(0u)
+                             : "memory");
+              }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          const bool whole = key0 + kChHalf - 1 <= pf &&
+                             (key0 >= low_last || key0 + kChHalf <= a.sinks) && good == all_ok;
+          ch_wait_ld();
+          if (!whole) {
+            // the row's keys, a bit each
+            const int hi = pos - key0, lo = low - key0, sk = a.sinks - key0;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t pages = ((good >> (2 * w)) & 1u ? 0xffffu : 0u) |
+                                     ((good >> (2 * w)) & 2u ? 0xffff0000u : 0u);
+              const uint32_t see = pg_below(hi + 1 - 32 * w) &
+                                   (~pg_below(lo - 32 * w) | pg_below(sk - 32 * w)) & pages;
+              // (most blocks of an edge tile are seen whole by all of the warp's rows)
+              if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!((see >> i) & 1u)) s[w * 32 + i] = 0xff800000u;
+              }
             }
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        const bool whole = key0 + kChHalf - 1 <= pf &&
-                           (key0 >= low_last || key0 + kChHalf <= a.sinks) && good == all_ok;
-        ch_wait_ld();
-        if (!whole) {
-          // the row's keys, a bit each
-          const int hi = pos - key0, lo = low - key0, sk = a.sinks - key0;
+          auto top = [&]() {
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t pages = ((good >> (2 * w)) & 1u ? 0xffffu : 0u) |
-                                   ((good >> (2 * w)) & 2u ? 0xffff0000u : 0u);
-            const uint32_t see = pg_below(hi + 1 - 32 * w) &
-                                 (~pg_below(lo - 32 * w) | pg_below(sk - 32 * w)) & pages;
-            // (most blocks of an edge tile are seen whole by all of the warp's rows)
-            if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+            for (int i = 0; i < kChHalf; i += 2)
+              mx4[(i >> 1) & 3] = ch_max3(mx4[(i >> 1) & 3], s[i], s[i + 1]);
+            return fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
+          };
+          uint64_t sum2[2];
+          auto weights = [&]() {
+            const float use = m == -INFINITY ? 0.f : m;
+            const uint64_t scale2 = pg_f2(a.scale_log2, a.scale_log2), neg2 = pg_f2(-use, -use);
+            sum2[0] = sum2[1] = 0ull;  // pairs of zeros
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((see >> i) & 1u)) s[w * 32 + i] = 0xff800000u;
+            for (int i = 0; i < 32; ++i) {
+              float p0, p1;
+              pg_split(pg_fma2(pg_u2(s[2 * i], s[2 * i + 1]), scale2, neg2), &p0, &p1);
+              p0 = pg_exp2(p0);
+              p1 = pg_exp2(p1);
+              sum2[i & 1] = pg_add2(sum2[i & 1], pg_f2(p0, p1));
+              p[i] = ch_pack(p0, p1);
             }
+          };
+          // The weights do not wait for the maximum: the reference rarely moves,
+          // and if it does they are taken again (the first half sets it first).
+          if (j == 0) m = top();
+          weights();
+          const float mx = top();
+          const bool raise = mx > m + kChLag || (m == -INFINITY && mx > m);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float mn = raise ? mx : m;
+            const float corr = raise ? exp2f(m - mn) : 1.f;  // 0 when m was none yet
+            m = mn;
+            l *= corr;
+            if (j > 0) {
+              // the product before this one has to finish (the one before that
+              // did before this buffer's scores were issued)
+              const uint32_t before = s_cnt - 1;
+              ok = ch_wait(&sm->pv_done[t][before & 1], (before >> 1) & 1, sm, a.status);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              ch_fence_after();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                ch_ld32(tO + c * 32, p);
+                ch_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) p[i] = __float_as_uint(__uint_as_float(p[i]) * corr);
+                ch_st32(tO + c * 32, p);
+              }
+            }
+            weights();
           }
+          ch_st32(tB, p);
+          float a0, a1;
+          pg_split(pg_add2(sum2[0], sum2[1]), &a0, &a1);
+          l += a0 + a1;
+          ch_wait_st();
+          ch_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->p_ready[t][buf]);
+          ++s_cnt;
         }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < kChHalf; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(s[i]));
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-        const bool raise = mx > m + kChLag || (m == -INFINITY && mx > m);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float mn = raise ? mx : m;
-          const float corr = raise ? exp2f(m - mn) : 1.f;  // 0 for the first half
-          m = mn;
-          l *= corr;
-          if (j > 0) {
-            // the product before this one has to finish (the one before that
-            // did before this buffer's scores were issued)
-            const uint32_t before = s_cnt - 1;
-            ok = ch_wait(&sm->pv_done[t][before & 1], (before >> 1) & 1, sm, a.status);
-            if (!__all_sync(0xffffffffu, ok)) {
-              ok = false;
-              break;
-            }
-            ch_fence_after();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              ch_ld32(tO + c * 32, p);
-              ch_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) p[i] = __float_as_uint(__uint_as_float(p[i]) * corr);
-              ch_st32(tO + c * 32, p);
-            }
-          }
-        }
-        const float use = m == -INFINITY ? 0.f : m;
-        const uint64_t scale2 = pg_f2(a.scale_log2, a.scale_log2), neg2 = pg_f2(-use, -use);
-        uint64_t sum2[2] = {0ull, 0ull};  // pairs of zeros
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float p0, p1;
-          pg_split(pg_fma2(pg_u2(s[2 * i], s[2 * i + 1]), scale2, neg2), &p0, &p1);
-          p0 = pg_exp2(p0);
-          p1 = pg_exp2(p1);
-          sum2[i & 1] = pg_add2(sum2[i & 1], pg_f2(p0, p1));
-          p[i] = ch_pack(p0, p1);
-        }
-        ch_st32(tB, p);
-        float a0, a1;
-        pg_split(pg_add2(sum2[0], sum2[1]), &a0, &a1);
-        l += a0 + a1;
-        ch_wait_st();
-        ch_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->p_ready[t][buf]);
-        ++s_cnt;
       }
       if (!ok) break;
       // ---- the piece's result ----------------------------------------------------------
