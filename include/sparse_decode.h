@@ -436,6 +436,7 @@ sparse_status_t sparse_paged_append(const sparse_paged_shape_t *shape, void *K, 
  * only those with j > p - window or j < sinks.  out [T,Hq,d], lse [T,Hq] or
  * NULL, as in sparse_attn_gather (nothing seen: o = 0, lse = -inf); padding
  * rows are left as they were.  K and V already hold the new tokens' rows.
+ * out and lse overlap neither each other nor q, K or V (refused).
  * A page id outside [0, num_pages) hides its tokens and raises
  * SPARSE_ERR_INDEX; a sequence with lengths outside the shape (rows outside
  * [0,T], more than max_new new tokens, a negative kv_len or one beyond its

@@ -92,6 +92,28 @@ def test_paged_calls_refuse_bad_pointers_and_sizes(lib):
     assert attn(nb=4096) == 3
 
 
+@pytest.mark.parametrize("T,stride", [(1, 512), (3, 512), (3, 1024)])
+def test_attn_refuses_results_over_its_inputs(lib, T, stride):
+    """Also where only the first or the last 16 bytes are shared."""
+    sh = _pshape(T=T)
+    es, n = (4, 2)[sh.dtype], ctypes.c_size_t(0)
+    assert lib.sparse_paged_workspace_size(ctypes.byref(sh), ctypes.byref(n)) == 0
+    row, A = sh.Hq * sh.d * es, 1 << 30
+    cache = sh.num_pages * sh.Hkv * sh.page_size * sh.d * es
+    p = lambda x: ctypes.c_void_p(x)
+    def attn(out, lse):
+        K, V, rest = A << 1, A << 2, A << 3
+        return lib.sparse_paged_attn(ctypes.byref(sh), p(A), stride, p(K), p(V), p(rest), p(rest),
+                                     p(rest), 0, 0, p(out), p(lse), p(rest), n.value, None)
+    q = (T - 1) * stride * es + row
+    for start, size in ((A, q), (A << 1, cache), (A << 2, cache)):
+        for out in (start, start + size - 16, start - T * row + 16):
+            assert attn(out, None) == 1
+        for lse in (start, start + size - 16, start - T * sh.Hq * 4 + 16):
+            assert attn(A << 4, lse) == 1
+    assert attn(A << 4, (A << 4) + T * row - 16) == 1
+
+
 def test_paged_python_refuses_host_tensors():
     K = torch.zeros(4, 2, 16, 64)
     i = torch.zeros(1, dtype=torch.int32)
@@ -109,7 +131,7 @@ def _i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def _batch(new, kv, Hq, Hkv, d, page, dtype, seed=0, pad=0, extra_cols=1, q_pad=0):
+def _batch(new, kv, Hq, Hkv, d, page, dtype, seed=0, pad=0, extra_cols=1, q_pad=0, grow=None):
     """A ragged batch over shuffled pages.  Everything that no sequence owns
     (page tails, spare pages, unused table entries) holds NaN or rubbish."""
     g = torch.Generator().manual_seed(seed)
@@ -123,7 +145,10 @@ def _batch(new, kv, Hq, Hkv, d, page, dtype, seed=0, pad=0, extra_cols=1, q_pad=
     V = torch.full((pages, Hkv, page, d), float("nan"), dtype=dtype)
     dense = []
     for b, c in enumerate(kv):
-        k = torch.randn(Hkv, max(c, 0), d, generator=g).to(dtype)
+        k = torch.randn(Hkv, max(c, 0), d, generator=g)
+        if grow is not None:
+            k *= grow(torch.arange(max(c, 0)))[:, None]
+        k = k.to(dtype)
         v = (torch.randn(Hkv, max(c, 0), d, generator=g) + 0.25).to(dtype)
         for j in range(nb[b]):
             pg = perm.pop()
@@ -336,6 +361,21 @@ def test_attn_long_runs(lib, dtype, d, page, new):
     """Runs of many tiles: every stage of a ring is reused several times."""
     x = _batch([new, 1], [30000, 17], 8, 8, d, page, dtype, seed=d + new)
     _assert_attn(x, sd.paged_attn(*x["args"], max_new=new))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 3, 150])
+@pytest.mark.parametrize("grow", [
+    lambda j: 0.02 * (j + 1.0),                # the maximum moves in every tile
+    lambda j: 0.001 + 60.0 * (j // 200),       # by more than fp32's range between two tiles
+    lambda j: 40.0 / (1 + j // 64),            # the first keys outweigh the rest
+], ids=["grows", "jumps", "falls"])
+def test_attn_scores_of_any_size(lib, dtype, d, new, grow):
+    x = _batch([new, min(new, 2)], [900, 413], 8, 2, d, 16, dtype, seed=d + new, grow=grow)
+    _assert_attn(x, sd.paged_attn(*x["args"], max_new=new))
+    _assert_attn(x, sd.paged_attn(*x["args"], max_new=new, window=333, sinks=5), 333, 5)
 
 
 @gpu
@@ -559,6 +599,9 @@ def test_python_refusals(lib):
             bad()
     with pytest.raises(sd.SparseDecodeError, match="UNSUPPORTED"):
         sd.paged_plan(kv, kv, table, kv, kv, 24, 1, 4)
+    for t in (q, q.contiguous()):  # the results over the queries
+        with pytest.raises((ValueError, sd.SparseDecodeError)):
+            sd.paged_attn(t, K, V, table, qs, kv, out=t)
     out, lse = sd.paged_attn(q[:0], K, V, table, _i32([0, 0]), kv)
     assert out.shape == (0, 8, 64) and lse.shape == (0, 8)
 

@@ -14,6 +14,10 @@ namespace sd {
 namespace {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 constexpr size_t kPagedHeader = 4096, kRunsOff = 3072, kTopsOff = 128, kGroupsOff = 192;
@@ -157,6 +161,17 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
   if (!ws || !sd::aligned(ws, 256)) return SPARSE_ERR_INVALID_ARG;
   const sd::PagedLayout l = sd::layout(s);
   if (ws_bytes < l.total) return SPARSE_ERR_WORKSPACE;
+  // results written while other blocks still read: never over the inputs
+  const size_t es = (size_t)s.esize(), o_bytes = (size_t)s.T * row * es;
+  const size_t q_bytes = ((size_t)(s.T - 1) * q_stride + row) * es;
+  const size_t c_bytes = (size_t)s.pages * s.Hkv * s.page * s.d * es;
+  const size_t l_bytes = lse ? (size_t)s.T * s.Hq * sizeof(float) : 0;
+  if (sd::overlap(out, o_bytes, q, q_bytes) || sd::overlap(out, o_bytes, K, c_bytes) ||
+      sd::overlap(out, o_bytes, V, c_bytes))
+    return SPARSE_ERR_INVALID_ARG;
+  if (lse && (sd::overlap(lse, l_bytes, q, q_bytes) || sd::overlap(lse, l_bytes, K, c_bytes) ||
+              sd::overlap(lse, l_bytes, V, c_bytes) || sd::overlap(lse, l_bytes, out, o_bytes)))
+    return SPARSE_ERR_INVALID_ARG;
   char *w = static_cast<char *>(ws);
   sd::PgArgs a;
   a.q = q;

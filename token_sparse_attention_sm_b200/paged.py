@@ -293,7 +293,7 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
     or j < ``sinks``.  max_new: the most new tokens one sequence has, if known
     (1 for a decode step: the kernels for few rows need it).  Returns
     (out [T,Hq,d], lse [T,Hq] or None); rows behind the last sequence are not
-    written."""
+    written.  ``out`` and ``lse`` overlap no other tensor of the call."""
     if ws is None:
         plain = _plain(q)
         if plain is not None and (max_new is None or max_new >= 1):
