@@ -788,9 +788,10 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   if (e == cudaSuccess) e = pg_cache_map(&mk, a.K, s, tile);
   if (e == cudaSuccess) e = pg_cache_map(&mv, a.V, s, tile);
   if (e != cudaSuccess) return e;
-  // starting a piece takes about as long as two tiles, a partial's way out and
-  // back another three
-  if ((e = launch_paged_schedule(s, a, 2 * TPT, kChKeys, di.sm_count, 8, 20, st)) != cudaSuccess)
+  // starting a piece takes about as long as two and a half tiles, a partial's
+  // way out and back nearly four more (2 and 5 in all: 94 us against 85 for 32
+  // tokens each of 8 sequences of 8K)
+  if ((e = launch_paged_schedule(s, a, 2 * TPT, kChKeys, di.sm_count, 10, 25, st)) != cudaSuccess)
     return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attrs[1];
