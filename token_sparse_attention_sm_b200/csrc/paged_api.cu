@@ -3,9 +3,9 @@
 // kernels on the caller's stream.
 //
 // Workspace: the 4 KB header with the device status word first and the decode
-// runs' arrival counters (zero between calls) from bytes 128 and 3072, the area that the
-// routing calls keep zero between calls (skipped, so that a workspace may serve
-// both), then the schedule and the partial results, which every call writes
+// runs' arrival counters (zero between calls) from bytes 128 and 3072, the area
+// that the routing calls keep zero between calls (skipped, so that a workspace
+// may serve both), then the schedule and the partial results, which every call writes
 // before reading.
 #include "paged.h"
 #include "paged.cuh"

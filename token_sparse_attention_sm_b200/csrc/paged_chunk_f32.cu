@@ -9,10 +9,10 @@
 // off by about 2^-22 |a b|.  The instruction's own sums are cut, not rounded, so
 // chains of them are kept short: the mixed products have accumulators of their
 // own, and a tile's share of O starts from zero and is added to O (one chain
-// over all keys was off by 3.9e-6 relative, this 4.2e-7).  Bound by those instructions, three for each product: a
-// 256-token chunk of 8,192 at d = 128, 32 query heads over 8, takes 837 us
-// (40 TFLOP/s; 1,265 with register-tiled multiply-adds), a 250-token chunk of
-// 4,096 at d = 64, 8 over 2, 74 us (96).
+// over all keys was off by 3.9e-6 relative, this 4.2e-7).  Bound by those
+// instructions, three for each product: a 256-token chunk of 8,192 at d = 128,
+// 32 query heads over 8, takes 837 us (40 TFLOP/s; 1,265 with register-tiled
+// multiply-adds), a 250-token chunk of 4,096 at d = 64, 8 over 2, 74 us.
 //
 // A worker (CTA) claims items of the schedule: a block of 128 query rows of one
 // (sequence, KV head), 16 per warp, and a piece of its 64-key tiles.  K and V
@@ -52,8 +52,7 @@ __device__ __forceinline__ void cf_ldsm4(const float *p, uint32_t *r) {
 }
 // x = hi + lo, hi x rounded to 11 significant bits (halves away from zero).
 // Rounded, not cut: a cut leaves lo with the sign of x, and the lo lo that is
-// dropped then adds up over the sum.  An addition and a
-// mask; the conversion instruction would run on the slow special-function unit.
+// dropped then adds up over the sum.  An addition and a mask; the conversion instruction would run on the slow special-function unit.
 __device__ __forceinline__ void cf_split(float x, uint32_t *hi, uint32_t *lo) {
   *hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   *lo = __float_as_uint(x - __uint_as_float(*hi));

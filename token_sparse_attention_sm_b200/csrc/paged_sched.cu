@@ -11,8 +11,8 @@
 // (the longest range cut into 1 .. 192 pieces): pieces per head P =
 // sum nrb * np, waves = ceil(P * Hkv / workers), cost = waves * (longest
 // piece + a fixed part for starting a piece and, when cut, for writing and
-// merging its partial: the caller's, in quarters of a tile).  The cheapest whose partials fit the workspace wins;
-// ties go to fewer pieces.  One CTA; latency bound (it also resets the call's
+// merging its partial: the caller's, in quarters of a tile).  The cheapest whose
+// partials fit the workspace wins; ties go to fewer pieces.  One CTA; latency bound (it also resets the call's
 // counters, so nothing of them has to be zero before a call).
 #include "paged.h"
 #include "paged.cuh"
