@@ -3,7 +3,7 @@
 // kernels on the caller's stream.
 //
 // Workspace: the 4 KB header with the device status word first and the decode
-// runs' arrival counters (zero between calls) from bytes 128 and 3072, the area
+// runs' arrival counters (zero between calls) from bytes 128 and 3328, the area
 // that the routing calls keep zero between calls (skipped, so that a workspace
 // may serve both), then the schedule and the partial results, which every call writes
 // before reading.
@@ -20,7 +20,7 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
 }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-constexpr size_t kPagedHeader = 4096, kRunsOff = 3072, kTopsOff = 128, kGroupsOff = 192;
+constexpr size_t kPagedHeader = 4096, kRunsOff = 3328, kTopsOff = 128, kGroupsOff = 192;
 static_assert(kTopsOff + kPagedTops * sizeof(uint32_t) <= kGroupsOff &&
                   kGroupsOff + kPagedMaxRuns * sizeof(uint32_t) <= 1024 &&
                   kRunsOff + kPagedMaxRuns * sizeof(uint32_t) <= kPagedHeader,
