@@ -66,7 +66,6 @@ struct PgArgs {
   uint32_t *runs;    // [kPagedMaxRuns] of a pair's runs, or its first group's, at its first run
   uint32_t *groups;  // [kPagedMaxRuns] of another group's runs, at the group's first run
   uint32_t *tops;    // [kPagedTops] of a pair's groups
-  uint32_t *arrive;  // [slot_cap * Hkv], zeroed by the schedule kernel
   float *part;       // [slot_cap * Hkv][part_rows][d] then [..][part_rows] (max, sum)
   int slot_cap;      // partial slots per KV head
   int part_rows;
@@ -151,15 +150,17 @@ __device__ __forceinline__ bool pg_lengths(const PgArgs &a, int b, int *row0, in
          (long long)c <= (long long)a.blocks * a.page;
 }
 
-// The sequence (and its schedule entry) that work item x of a head is in:
-// the last one with base <= x.  One warp, 32 probes a round.
-__device__ __forceinline__ int pg_find(const PgSeq *seqs, int B, int x, PgSeq *out) {
+// The sequence (and its schedule entry) that work item (`of` = &PgSeq::base) or
+// partial slot (&PgSeq::slot) x of a head is in: the last one that starts at x or
+// before.  One warp, 32 probes a round.
+__device__ __forceinline__ int pg_find(const PgSeq *seqs, int B, int x, int PgSeq::*of,
+                                       PgSeq *out) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, n = B;  // seqs[lo].base <= x < seqs[lo + n].base
+  int lo = 0, n = B;  // seqs[lo] starts at x or before, seqs[lo + n] after it
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int at = min(lo + lane * step, lo + n);
-    const bool le = seqs[at].base <= x && at < lo + n;
+    const bool le = seqs[at].*of <= x && at < lo + n;
     const uint32_t m = __ballot_sync(0xffffffffu, le);
     const int k = __popc(m) - 1;
     const int nlo = lo + k * step;

@@ -18,7 +18,7 @@ constexpr int kPagedMaxB = 4096;  // sequences a call may have
 
 // Workspace of the attention: the schedule, then the partials.
 struct PagedLayout {
-  size_t head_off, seqs_off, arrive_off, part_off, total;
+  size_t head_off, seqs_off, part_off, total;
   int slot_cap, part_rows;
 };
 
@@ -38,5 +38,7 @@ cudaError_t launch_paged_chunk_f32(const PagedShape &s, const PgArgs &a, cudaStr
 // quarters of a tile (paged_sched.cu).
 cudaError_t launch_paged_schedule(const PagedShape &s, const PgArgs &a, int tb, int kt, int grid,
                                   int whole_cost, int cut_cost, cudaStream_t st);
+// Joins the partials of the cut ranges (paged_merge.cu), row blocks of `tb` tokens.
+cudaError_t launch_paged_merge(const PagedShape &s, const PgArgs &a, int tb, cudaStream_t st);
 
 }  // namespace sd

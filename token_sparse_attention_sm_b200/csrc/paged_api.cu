@@ -59,9 +59,8 @@ PagedLayout layout(const PagedShape &s) {
   l.part_rows = (int)(rows < 256 ? rows : 256);
   l.head_off = kPagedScratch;
   l.seqs_off = l.head_off + up256(sizeof(PgHead));
-  l.arrive_off = l.seqs_off + up256((size_t)(s.B + 1) * sizeof(PgSeq));
   // partials: slot_cap * Hkv >= kPartialSlots >= 2 * kPagedMaxRuns
-  l.part_off = l.arrive_off + up256((size_t)l.slot_cap * s.Hkv * sizeof(uint32_t));
+  l.part_off = l.seqs_off + up256((size_t)(s.B + 1) * sizeof(PgSeq));
   l.total = l.part_off + up256((size_t)l.slot_cap * s.Hkv * l.part_rows * (s.d + 2) *
                                sizeof(float));
   return l;
@@ -203,7 +202,6 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
   a.runs = reinterpret_cast<uint32_t *>(w + sd::kRunsOff);
   a.groups = reinterpret_cast<uint32_t *>(w + sd::kGroupsOff);
   a.tops = reinterpret_cast<uint32_t *>(w + sd::kTopsOff);
-  a.arrive = reinterpret_cast<uint32_t *>(w + l.arrive_off);
   a.part = reinterpret_cast<float *>(w + l.part_off);
   a.slot_cap = l.slot_cap;
   a.part_rows = l.part_rows;

@@ -70,7 +70,7 @@ struct ChItem {
   int p_first, p_last, low;            // positions of its first and last token; lowest key of a window
   int u0, u1, halves;                  // the piece's tiles, and the 64-key halves to run
   int sink_tiles, lo;
-  int np, piece, first;                // partial slots: (first + piece) * Hkv + h
+  int np, slot;                        // pieces of the range; its partial: slot * Hkv + h
   int valid;                           // 0: no more items
 };
 
@@ -80,11 +80,11 @@ struct ChSmall {
   // [row tile][S buffer]: a buffer's phases alternate strictly, so a parity
   // wait is never two phases off
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];
-  uint64_t o_empty[2], wg[2];
+  uint64_t o_empty[2];
   uint64_t item_full[2], item_empty[2];
   ChItem item[2];
   uint32_t ok[8];
-  uint32_t tmem, abort, last[2];
+  uint32_t tmem, abort;
 };
 static_assert(sizeof(ChSmall) <= 1024, "small area");
 
@@ -233,7 +233,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
         mbar_init(&sm->pv_done[t][i], 1);
       }
       mbar_init(&sm->o_empty[t], 4);
-      mbar_init(&sm->wg[t], 4);
       mbar_init(&sm->item_full[t], 1);
       mbar_init(&sm->item_empty[t], kChSoftWarps + 3);
     }
@@ -278,7 +277,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (valid) {
             const int y = (int)(x % (uint32_t)per_head);
             PgSeq sq;
-            const int b = pg_find(a.seqs, a.B, y, &sq);
+            const int b = pg_find(a.seqs, a.B, y, &PgSeq::base, &sq);
             if (lane == 0) {
               int row0, n, kv;
               pg_lengths(a, b, &row0, &n, &kv);
@@ -306,8 +305,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                   t.tile(I.u1 - 1) * kChKeys + kChHalf > p_last)
                 --I.halves;
               I.np = sq.np;
-              I.piece = piece;
-              I.first = sq.slot + rb * sq.np;
+              I.slot = sq.slot + rb * sq.np + piece;
             }
           }
           if (lane == 0) {
@@ -513,20 +511,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
     const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + 256 + t * 128;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
     int ring = 0;  // ring position of the next K tile, and the phase of its round
-    uint32_t phase = 0, s_cnt = 0, wg_cnt = 0;
+    uint32_t phase = 0, s_cnt = 0;
     int unit = 0;
     bool ok = true;
     constexpr uint32_t all_ok = (1u << (kChHalf / 16)) - 1u;
     auto step = [&]() {
       if (++ring == C::kSlots) ring = 0, phase ^= 1u;
-    };
-    // the four warps of the tile meet (bounded)
-    auto wg_sync = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->wg[t]);
-      const bool w = ch_wait(&sm->wg[t], wg_cnt & 1, sm, a.status);
-      ++wg_cnt;
-      return w;
     };
     for (int it = 0;; ++it) {
       if (!ch_wait(&sm->item_full[it & 1], (it >> 1) & 1, sm, a.status)) break;
@@ -702,8 +692,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       const size_t at = (size_t)(I.row0 + I.t0 + a.by_G(br)) * a.Hq + I.h * G + br - a.by_G(br) * G;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const size_t per = (size_t)a.part_rows * D;
-      const size_t first = (size_t)I.first * a.Hkv + I.h;
-      const size_t mine = first + (size_t)I.piece * a.Hkv;
+      const size_t mine = (size_t)I.slot * a.Hkv + I.h;
       float2 *ml = reinterpret_cast<float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -745,22 +734,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
         continue;
       }
       if (live) ml[mine * a.part_rows + br] = make_float2(m, l);
-      __threadfence();
-      if (!(ok = wg_sync())) break;
-      if (tid % 128 == 0)
-        sm->last[t] = atomicAdd(&a.arrive[first + (size_t)t * a.Hkv], 1u) == (uint32_t)(I.np - 1);
-      if (!(ok = wg_sync())) break;
-      if (sm->last[t]) {
-        // the block's last piece to arrive merges them all
-        __threadfence();
-        pg_merge<D, 4>(a, first, I.np, t * tile_rows, min(I.rows - t * tile_rows, tile_rows), r, 128,
-                    [&](int row) {
-                      return (size_t)(I.row0 + I.t0 + a.by_G(row)) * a.Hq + I.h * G + row -
-                             a.by_G(row) * G;
-                    },
-                    out);
-      }
-      if (!(ok = wg_sync())) break;  // sm->last is read before the next item's
       done();
     }
   }
@@ -802,8 +775,8 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.numAttrs = 0;
   add_pdl_attr(cfg, attrs);
-  e = cudaLaunchKernelEx(&cfg, kern, a, mq, mk, mv, tile);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  if ((e = cudaLaunchKernelEx(&cfg, kern, a, mq, mk, mv, tile)) != cudaSuccess) return e;
+  return launch_paged_merge(s, a, 2 * TPT, st);
 }
 
 }  // namespace

@@ -11,8 +11,8 @@
 // own, and a tile's share of O starts from zero and is added to O (one chain
 // over all keys was off by 3.9e-6 relative, this 4.2e-7).  Bound by those
 // instructions, three for each product: a 256-token chunk of 8,192 at d = 128,
-// 32 query heads over 8, takes 837 us (40 TFLOP/s; 1,265 with register-tiled
-// multiply-adds), a 250-token chunk of 4,096 at d = 64, 8 over 2, 74 us.
+// 32 query heads over 8, takes 817 us (41 TFLOP/s; 1,265 with register-tiled
+// multiply-adds), a 250-token chunk of 4,096 at d = 64, 8 over 2, 70 us.
 //
 // A worker (CTA) claims items of the schedule: a block of 128 query rows of one
 // (sequence, KV head), 16 per warp, and a piece of its 64-key tiles.  K and V
@@ -21,8 +21,8 @@
 // conflicts.  The weights go from the accumulators of S straight into the
 // operand of the second product: its inner index runs over the keys in the
 // order 0 2 4 6 1 3 5 7, which is how a lane already holds them.  A piece of a
-// cut range writes (O, m, l) to its slot; the last piece of the block to arrive
-// merges them in piece order.
+// cut range writes (O, m, l) to its slot, which the merge kernel joins in piece
+// order.
 #include "paged.h"
 #include "paged.cuh"
 
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     if (item >= (long long)per_head * a.Hkv) break;
     const int h = (int)(item / per_head), x = (int)(item % per_head);
     PgSeq sq;
-    const int b = pg_find(a.seqs, a.B, x, &sq);
+    const int b = pg_find(a.seqs, a.B, x, &PgSeq::base, &sq);
     int row0, n, kv;
     pg_lengths(a, b, &row0, &n, &kv);
     const int nrb = (n + TB - 1) / TB;
@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(kCfThreads, 1)
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
-    const size_t first = (size_t)(sq.slot + rb * sq.np) * a.Hkv;  // slots (piece, head)
-    const size_t per = (size_t)a.part_rows * D, mine = first + (size_t)piece * a.Hkv + h;
+    const size_t per = (size_t)a.part_rows * D;
+    const size_t mine = (size_t)(sq.slot + rb * sq.np + piece) * a.Hkv + h;  // its partial
     float2 *ml = reinterpret_cast<float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -309,18 +309,6 @@ __global__ void __launch_bounds__(kCfThreads, 1)
         if (!whole) ml[mine * a.part_rows + r] = make_float2(m[i], l[i]);
         else if (a.lse)
           a.lse[place(r)] = l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
-      }
-    }
-    if (sq.np > 1) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) box[0] = atomicAdd(&a.arrive[first + h], 1u) == (uint32_t)(sq.np - 1);
-      __syncthreads();
-      const bool last = box[0] != 0;
-      __syncthreads();
-      if (last) {
-        __threadfence();
-        pg_merge<D, 4>(a, first + h, sq.np, 0, rows, tid, kCfThreads, place, out);
       }
     }
     __syncthreads();
@@ -349,8 +337,8 @@ cudaError_t run(const PagedShape &s, const PgArgs &a, cudaStream_t st) {
   cfg.attrs = attrs;
   cfg.numAttrs = 0;
   add_pdl_attr(cfg, attrs);
-  e = cudaLaunchKernelEx(&cfg, kern, a);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  if ((e = cudaLaunchKernelEx(&cfg, kern, a)) != cudaSuccess) return e;
+  return launch_paged_merge(s, a, kCfRows / s.G(), st);
 }
 
 }  // namespace

@@ -12,8 +12,8 @@
 // sum nrb * np, waves = ceil(P * Hkv / workers), cost = waves * (longest
 // piece + a fixed part for starting a piece and, when cut, for writing and
 // merging its partial: the caller's, in quarters of a tile).  The cheapest whose
-// partials fit the workspace wins; ties go to fewer pieces.  One CTA; latency bound (it also resets the call's
-// counters, so nothing of them has to be zero before a call).
+// partials fit the workspace wins; ties go to fewer pieces.  One CTA; latency bound (it also sets the call's
+// claim counter, which needs no value before a call).
 #include "paged.h"
 #include "paged.cuh"
 
@@ -103,10 +103,7 @@ __global__ void __launch_bounds__(kScThreads) paged_schedule_kernel(const PgArgs
     }
   }
   __syncthreads();
-  if (warp > 0) {
-    for (int i = tid - 32; i < a.slot_cap * a.Hkv; i += kScThreads - 32) a.arrive[i] = 0u;
-    return;
-  }
+  if (warp > 0) return;
   // the cheapest (one piece needs no slot: always possible)
   unsigned long long cost = s_cost[lane];
   int best = lane;
