@@ -380,6 +380,23 @@ def test_attn_scores_of_any_size(lib, dtype, d, new, grow):
 
 @gpu
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new", [[1, 1], [2, 60]])
+def test_attn_pages_in_several_places(lib, dtype, new):
+    """Two sequences that share their first pages, and a page that stands twice
+    in one sequence."""
+    x = _batch(new, [300, 210], 8, 2, 128, 16, dtype, seed=5)
+    table = x["args"][3]
+    table[1, :6] = table[0, :6]
+    table[0, 9] = table[0, 3]
+    for (k0, k1) in zip(*x["dense"]):
+        k1[:, :96] = k0[:, :96]
+        k0[:, 144:160] = k0[:, 48:64]
+    _assert_attn(x, sd.paged_attn(*x["args"], max_new=max(new)))
+    _assert_attn(x, sd.paged_attn(*x["args"], max_new=max(new), window=150, sinks=20), 150, 20)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_attn_rows_that_see_nothing(lib, dtype):
     # more new tokens than cached ones: the first rows stand before the cache
     x = _batch([5, 3, 200, 1], [2, 0, 150, 0], 8, 2, 64, 16, dtype)
@@ -507,6 +524,18 @@ def test_plan(lib, new, lens, page, T):
     p = sd.paged_plan(nl, ln, tab, free, fc, page, T, pages, kv_lens=ln, free_left=fc)
     assert ln.tolist() == want[1] and fc.tolist() == [len(want[5])]
     assert p["slots"].tolist() == want[4]
+
+
+@gpu
+@pytest.mark.parametrize("T", [0, 3])
+@pytest.mark.parametrize("free", [[], [4, 2]])
+def test_plan_of_nothing(lib, T, free):
+    """No new tokens, an empty free list, no rows."""
+    table = _i32([[1, -1], [0, 3]])
+    p = sd.paged_plan(_i32([0, 0]), _i32([16, 20]), table, _i32(free), _i32([len(free)]), 16, T, 5)
+    assert p["kv_lens"].tolist() == [16, 20] and p["q_start"].tolist() == [0, 0, 0]
+    assert p["positions"].tolist() == [-1] * T and p["slots"].tolist() == [-1] * T
+    assert p["free_left"].tolist() == [len(free)] and table.tolist() == [[1, -1], [0, 3]]
 
 
 @gpu
