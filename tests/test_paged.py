@@ -12,6 +12,8 @@ Z = max_j sum_i |q_i k_ji| / sqrt(d):
   (2^-8 |o|)."""
 import ctypes
 import math
+import threading
+import time
 
 import pytest
 import torch
@@ -744,3 +746,93 @@ def test_calls_on_two_streams(lib):
         assert torch.equal(a[0], gx[0][0]) and torch.equal(a[1], gx[0][1])
     for a in gy:
         assert torch.equal(a[0], gy[0][0]) and torch.equal(a[1], gy[0][1])
+
+
+# ---- host threads that share a stream ------------------------------------------------------
+
+class _HostPaged:
+    """paged.py on host tensors, its C calls replaced by ones that record when
+    they begin and end and let other threads run in between, as ctypes does."""
+
+    def __init__(self, monkeypatch):
+        from token_sparse_attention_sm_b200 import paged
+        self.log, self.paged = [], paged
+        monkeypatch.setattr(paged, "_stream_ws", {})
+        monkeypatch.setattr(paged, "Workspace", lambda dev: sd.Workspace("cpu"))
+        monkeypatch.setattr(paged, "_one_device", lambda *ts: 0)
+        monkeypatch.setattr(paged, "_entry", lambda name: self.call)
+        monkeypatch.setattr(paged, "_calls", lambda: self)
+        monkeypatch.setattr(paged, "_plain", self.plain)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0)
+        monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False)
+
+    def call(self, *a):
+        me = threading.get_ident()
+        for _ in range(3):  # a schedule, its items, the merge
+            self.log.append(me)
+            time.sleep(0.002)
+        return 0
+
+    def attn(self, *a):  # the compiled form holds the global lock: no sleep
+        self.log.extend([threading.get_ident()] * 3)
+        return None, None
+
+    def plain(self, t):
+        ws = self.paged._stream_ws.get((0, 0))
+        return (self, ws, 0) if ws is not None and t.shape[0] == 1 else None
+
+    def together(self, *calls):
+        errors = []
+        def run(f):
+            try:
+                for _ in range(5):
+                    time.sleep(0.001)
+                    f()
+            except Exception as e:  # pragma: no cover
+                errors.append(e)
+        ts = [threading.Thread(target=run, args=(f,)) for f in calls]
+        [t.start() for t in ts]
+        [t.join() for t in ts]
+        assert not errors
+        assert len(self.log) == 15 * len(calls)
+        for i in range(0, len(self.log), 3):
+            assert len(set(self.log[i:i + 3])) == 1, "the launches of two calls are mixed"
+
+
+def _host_attn(B, T):
+    K = torch.zeros(4, 2, 16, 64)
+    i = torch.zeros(B, dtype=torch.int32)
+    return lambda: sd.paged_attn(torch.zeros(T, 8, 64), K, K, i[:, None].contiguous(),
+                                 torch.zeros(B + 1, dtype=torch.int32), i, check=False)
+
+
+def test_threads_on_one_stream_do_not_mix_their_launches(monkeypatch, lib):
+    h = _HostPaged(monkeypatch)
+    # other batches, workspaces that grow, the compiled form among them
+    h.together(_host_attn(2, 40), _host_attn(3, 300), _host_attn(1, 1))
+
+
+@gpu
+def test_attn_from_threads_of_one_stream(lib):
+    xs = [_batch([1, 20], [4000, 3000], 8, 2, 128, 16, BF16, seed=7),
+          _batch([300, 2, 5], [2500, 70, 900], 8, 1, 128, 16, BF16, seed=8),
+          _batch([1] * 9, [100 * i + 5 for i in range(9)], 8, 2, 128, 16, BF16, seed=9)]
+    torch.cuda.synchronize()
+    sd.paged._stream_ws.clear()  # the first calls make and grow it
+    got, errors = [[] for _ in xs], []
+    def run(i):
+        try:
+            for _ in range(20):
+                got[i].append(sd.paged_attn(*xs[i]["args"], max_new=max(xs[i]["new"]),
+                                            check=False))
+        except Exception as e:  # pragma: no cover
+            errors.append(e)
+    ts = [threading.Thread(target=run, args=(i,)) for i in range(3)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    torch.cuda.synchronize()
+    assert not errors
+    for x, g in zip(xs, got):
+        _assert_attn(x, g[0])
+        assert all(torch.equal(a[0], g[0][0]) and torch.equal(a[1], g[0][1]) for a in g)

@@ -16,7 +16,8 @@ A serving step is ``paged_plan`` once, then per layer ``paged_append`` and
     out, lse = sd.paged_attn(q, K, V, table, p["q_start"], p["kv_lens"])
     lens, free_count = p["kv_lens"], p["free_left"]
 
-Without ``ws`` a call uses a workspace kept for its device and stream; inside
+Without ``ws`` a call uses a workspace kept for its device and stream, which
+host threads may share: a call's kernels are enqueued under its lock.  Inside
 a stream capture it takes one from the graph's own memory instead, so two
 captured graphs never share scratch.  Calls given one Workspace are ordered by
 the caller, and a capture needs it to be large enough already.  ``check``
@@ -28,6 +29,7 @@ import ctypes
 import functools
 import importlib.util
 import os
+import threading
 
 import torch
 
@@ -111,16 +113,31 @@ def _one_device(t, *ts) -> int:
     raise ValueError("all tensors must be on one device")
 
 
-def _scratch(ws: Workspace | None, dev: int, nbytes: int, check: bool):
-    """The workspace of one call on the current device: the buffer, and the
-    current stream."""
+def _kept(dev: int, stream: int) -> Workspace:
+    """The workspace kept for a device's stream.  An attention is up to three
+    kernels over one schedule and its partials, and the C call that enqueues
+    them runs without Python's global lock, so threads that share a stream take
+    turns under the workspace's own lock, from its growth to the last launch."""
+    ws = _stream_ws.get((dev, stream))
+    if ws is None:
+        ws = Workspace(f"cuda:{dev}")
+        ws.lock = threading.RLock()
+        ws.get(_HEADER)  # whoever finds it finds a buffer
+        ws = _stream_ws.setdefault((dev, stream), ws)
+    return ws
+
+
+def _launch(what: str, ws: Workspace | None, dev: int, nbytes: int, check: bool, call):
+    """One call on the current device and stream: call(buffer address, bytes,
+    stream) with a workspace of nbytes, then its status."""
     stream = torch._C._cuda_getCurrentRawStream(dev)
     capturing = torch._C._cuda_isCurrentStreamCapturing()
     if ws is None and not capturing:
-        ws = _stream_ws.get((dev, stream))
-        if ws is None:
-            ws = _stream_ws[dev, stream] = Workspace(f"cuda:{dev}")
-        return ws, ws.get(nbytes), stream
+        ws = _kept(dev, stream)
+        with ws.lock:
+            buf = ws.get(nbytes)
+            rc = call(buf.data_ptr(), buf.numel(), stream)
+        return _finish(rc, what, ws, check)
     if capturing and check:
         raise ValueError("check=True synchronises: give check=False inside a stream capture")
     if ws is None:
@@ -128,7 +145,7 @@ def _scratch(ws: Workspace | None, dev: int, nbytes: int, check: bool):
         buf = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
         if nbytes > _HEADER:
             buf[:_HEADER].zero_()
-        return None, buf, stream
+        return _finish(call(buf.data_ptr(), nbytes, stream), what, None, check)
     if ws.device.index not in (None, dev):
         raise ValueError(f"workspace on {ws.device}, tensors on cuda:{dev}")
     if capturing:
@@ -137,7 +154,8 @@ def _scratch(ws: Workspace | None, dev: int, nbytes: int, check: bool):
                              f"get({nbytes}) before it")
         # the graph keeps this address, also when ws grows later
         ws.kept = getattr(ws, "kept", []) + [ws.buf]
-    return ws, ws.get(nbytes), stream
+    buf = ws.get(nbytes)
+    return _finish(call(buf.data_ptr(), buf.numel(), stream), what, ws, check)
 
 
 def _finish(rc: int, what: str, ws, check: bool):
@@ -199,8 +217,9 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
         plain = _plain(new_lens)
         if plain is not None:
             calls, w, stream = plain
-            r = calls.plan(w.buf, stream, new_lens, lens, block_table, free_pages, free_count,
-                           int(page_size), int(num_tokens), int(num_pages), kv_lens, free_left)
+            with w.lock:
+                r = calls.plan(w.buf, stream, new_lens, lens, block_table, free_pages, free_count,
+                               int(page_size), int(num_tokens), int(num_pages), kv_lens, free_left)
             if type(r) is tuple:
                 _finish(0, "paged_plan", w, check)
                 return {"kv_lens": r[0], "q_start": r[1], "positions": r[2], "slots": r[3],
@@ -231,18 +250,16 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
             return paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size,
                               num_tokens, num_pages, ws, check, kv_lens, q_start, positions, slots,
                               free_left)
-    w, buf, stream = _scratch(ws, dev, _HEADER, check)
     # one allocation for the results that were not given
     want = [n for t, n in zip(res, sizes) if t is None]
     if want:
         new = iter(torch.empty(sum(want), dtype=_I32, device=new_lens.device).split(want))
         res = [next(new) if t is None else t for t in res]
     positions, slots, kv_lens, q_start, free_left = res
-    _finish(_entry("sparse_paged_plan")(
+    _launch("paged_plan", ws, dev, _HEADER, check, lambda at, n, stream: _entry("sparse_paged_plan")(
         sh, new_lens.data_ptr(), lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), F,
         free_count.data_ptr(), kv_lens.data_ptr(), q_start.data_ptr(), positions.data_ptr(),
-        slots.data_ptr(), free_left.data_ptr(), buf.data_ptr(), buf.numel(), stream),
-        "paged_plan", w, check)
+        slots.data_ptr(), free_left.data_ptr(), at, n, stream))
     return {"kv_lens": kv_lens, "q_start": q_start, "positions": positions, "slots": slots,
             "free_left": free_left}
 
@@ -256,7 +273,8 @@ def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: 
         plain = _plain(K)
         if plain is not None:
             calls, w, stream = plain
-            r = calls.append(w.buf, stream, K, V, k_new, v_new, slots)
+            with w.lock:
+                r = calls.append(w.buf, stream, K, V, k_new, v_new, slots)
             if r is not None:
                 return _finish(r, "paged_append", w, check)
     dev = _one_device(K, V, k_new, v_new, slots)
@@ -274,10 +292,10 @@ def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: 
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return paged_append(K, V, k_new, v_new, slots, ws, check)
-    w, buf, stream = _scratch(ws, dev, _HEADER, check)
-    _finish(_entry("sparse_paged_append")(
-        sh, K.data_ptr(), V.data_ptr(), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
-        slots.data_ptr(), buf.data_ptr(), buf.numel(), stream), "paged_append", w, check)
+    _launch("paged_append", ws, dev, _HEADER, check,
+            lambda at, n, stream: _entry("sparse_paged_append")(
+                sh, K.data_ptr(), V.data_ptr(), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+                slots.data_ptr(), at, n, stream))
 
 
 def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: int = 0,
@@ -298,8 +316,9 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
         plain = _plain(q)
         if plain is not None and (max_new is None or max_new >= 1):
             calls, w, stream = plain
-            r = calls.attn(w.buf, stream, q, K, V, block_table, q_start, kv_lens, int(window),
-                           int(sinks), int(max_new or 0), return_lse, out, lse)
+            with w.lock:
+                r = calls.attn(w.buf, stream, q, K, V, block_table, q_start, kv_lens, int(window),
+                               int(sinks), int(max_new or 0), return_lse, out, lse)
             if type(r) is tuple:
                 _finish(0, "paged_attn", w, check)
                 return r
@@ -337,10 +356,8 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
         lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
     if T == 0:
         return out, lse
-    w, buf, stream = _scratch(ws, dev, nbytes, check)
-    _finish(_entry("sparse_paged_attn")(
+    _launch("paged_attn", ws, dev, nbytes, check, lambda at, n, stream: _entry("sparse_paged_attn")(
         sh, q.data_ptr(), qs, K.data_ptr(), V.data_ptr(), block_table.data_ptr(),
         q_start.data_ptr(), kv_lens.data_ptr(), window, sinks, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), stream),
-        "paged_attn", w, check)
+        None if lse is None else lse.data_ptr(), at, n, stream))
     return out, lse
