@@ -35,7 +35,8 @@
 // sum is taken before the rounding.
 //
 // Every wait is bounded; when one runs out the kernel raises TIMEOUT, all
-// roles leave their loops, the tensor memory is freed and the kernel returns.
+// roles leave their loops, each waits for what it still has in flight (copies,
+// products, loads), the tensor memory is freed and the kernel returns.
 #include "paged.h"
 #include "paged.cuh"
 #include "paged_tma.h"
@@ -400,6 +401,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       // last kSlots positions of the ring: an older slot has moved on)
       for (int at = 2 * unit - 2 + isV; at >= max(0, 2 * unit - C::kSlots); at -= 2)
         mbar_wait(&sm->full[at % C::kSlots], (at / C::kSlots) & 1, a.status);
+      if (q_count > 0) mbar_wait(&sm->q_full, (q_count - 1) & 1, a.status);
     } else {
       // ---- MMA warps, one per row tile: all lanes walk, one issues ---------------------
       // (The walk stays uniform and the issue under elect.sync, so the operands
@@ -501,6 +503,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
           ++p_cnt;
         }
       }
+      // and its products, before their tensor memory is freed
+      if (s_cnt > 0)
+        mbar_wait(&sm->s_full[t][(s_cnt - 1) & 1], ((s_cnt - 1) >> 1) & 1, a.status);
+      if (p_cnt > 0)
+        mbar_wait(&sm->pv_done[t][(p_cnt - 1) & 1], ((p_cnt - 1) >> 1) & 1, a.status);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChSoftRegs));
@@ -519,7 +526,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
       if (++ring == C::kSlots) ring = 0, phase ^= 1u;
     };
     for (int it = 0;; ++it) {
-      if (!ch_wait(&sm->item_full[it & 1], (it >> 1) & 1, sm, a.status)) break;
+      // the warp leaves together: its lanes meet again in the collectives below
+      if (!__all_sync(0xffffffffu,
+                      ch_wait(&sm->item_full[it & 1], (it >> 1) & 1, sm, a.status)))
+        break;
       const ChItem &I = sm->item[it & 1];  // until this warp's arrival below
       auto done = [&]() {
         __syncwarp();
@@ -736,6 +746,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
       if (live) ml[mine * a.part_rows + br] = make_float2(m, l);
       done();
     }
+    ch_wait_ld();
+    ch_wait_st();
   }
   ch_fence_before();
   __syncthreads();
