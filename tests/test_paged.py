@@ -751,8 +751,8 @@ def test_calls_on_two_streams(lib):
 # ---- host threads that share a stream ------------------------------------------------------
 
 class _HostPaged:
-    """paged.py on host tensors, its C calls replaced by ones that record when
-    they begin and end and let other threads run in between, as ctypes does."""
+    """paged.py on host tensors, its C calls replaced by ones that note their
+    launches and let other threads run in between."""
 
     def __init__(self, monkeypatch):
         from token_sparse_attention_sm_b200 import paged
@@ -761,8 +761,7 @@ class _HostPaged:
         monkeypatch.setattr(paged, "Workspace", lambda dev: sd.Workspace("cpu"))
         monkeypatch.setattr(paged, "_one_device", lambda *ts: 0)
         monkeypatch.setattr(paged, "_entry", lambda name: self.call)
-        monkeypatch.setattr(paged, "_calls", lambda: self)
-        monkeypatch.setattr(paged, "_plain", self.plain)
+        monkeypatch.setattr(paged, "_plain", lambda t: None)
         monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0)
         monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False)
@@ -773,14 +772,6 @@ class _HostPaged:
             self.log.append(me)
             time.sleep(0.002)
         return 0
-
-    def attn(self, *a):  # the compiled form holds the global lock: no sleep
-        self.log.extend([threading.get_ident()] * 3)
-        return None, None
-
-    def plain(self, t):
-        ws = self.paged._stream_ws.get((0, 0))
-        return (self, ws, 0) if ws is not None and t.shape[0] == 1 else None
 
     def together(self, *calls):
         errors = []
@@ -809,8 +800,17 @@ def _host_attn(B, T):
 
 def test_threads_on_one_stream_do_not_mix_their_launches(monkeypatch, lib):
     h = _HostPaged(monkeypatch)
-    # other batches, workspaces that grow, the compiled form among them
-    h.together(_host_attn(2, 40), _host_attn(3, 300), _host_attn(1, 1))
+    h.together(_host_attn(2, 40), _host_attn(3, 300), _host_attn(1, 1))  # it grows
+
+
+@pytest.mark.parametrize("name", ["plan", "append", "attn"])
+def test_c_calls_keep_the_global_lock(lib, name):
+    """No other thread's launches can come between those of one call, the
+    compiled calls' (which take no other lock) among them."""
+    from token_sparse_attention_sm_b200 import paged
+    fn = paged._entry(f"sparse_paged_{name}")
+    assert fn._flags_ & 4  # ctypes' FUNCFLAG_PYTHONAPI
+    assert fn.argtypes == getattr(lib, f"sparse_paged_{name}").argtypes
 
 
 @gpu

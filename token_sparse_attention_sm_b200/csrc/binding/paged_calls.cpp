@@ -2,10 +2,12 @@
 // the checks: a decode step's kernels take a few microseconds, and checking a
 // dozen tensors and allocating the results from Python took ten more.
 //
-// Each function takes the caller's tensors, the stream's workspace buffer and
-// the stream, and returns the results when every argument is as the C entry
-// point wants it; otherwise it returns None, having done nothing, and paged.py
-// goes through the arguments itself and says what is wrong.  The C entry points
+// Each function takes the caller's tensors, the stream's workspace (its buffer
+// is read here, and no other thread can replace it before the launches: the
+// global lock is held throughout) and the stream, and returns the results when
+// every argument is as the C entry point wants it; otherwise it returns None,
+// having done nothing, and paged.py goes through the arguments itself and says
+// what is wrong.  The C entry points
 // are handed over by address (bind), so this module links against nothing of
 // the library's; a status other than OK comes back as an int.
 #include <torch/csrc/autograd/python_variable.h>
@@ -25,6 +27,14 @@ Attn g_attn;
 Size g_size;
 
 py::object none() { return py::none(); }
+
+// the buffer a paged.py workspace has now
+at::Tensor buffer(const py::object &ws) {
+  static PyObject *name = PyUnicode_InternFromString("buf");
+  const auto buf = py::reinterpret_steal<py::object>(PyObject_GetAttr(ws.ptr(), name));
+  if (!buf) throw py::error_already_set();
+  return py::cast<at::Tensor>(buf);
+}
 
 // a dense int32 tensor of this device
 bool ints(const at::Tensor &t, const at::Device &dev, int64_t dims) {
@@ -55,13 +65,14 @@ bool caches(const at::Tensor &K, const at::Tensor &V) {
 }
 
 
-py::object attn(const at::Tensor &buf, int64_t stream, const at::Tensor &q, const at::Tensor &K,
+py::object attn(const py::object &ws, int64_t stream, const at::Tensor &q, const at::Tensor &K,
                 const at::Tensor &V, const at::Tensor &table, const at::Tensor &q_start,
                 const at::Tensor &kv_lens, int64_t window, int64_t sinks, int64_t max_new,
                 bool want_lse, const c10::optional<at::Tensor> &out_given,
                 const c10::optional<at::Tensor> &lse_given) {
   if (!caches(K, V) || q.scalar_type() != K.scalar_type() || q.dim() != 3) return none();
   const at::Device dev = K.device();
+  const at::Tensor buf = buffer(ws);
   const int64_t T = q.size(0), Hq = q.size(1), d = K.size(3);
   const int64_t qs = row_stride(q, dev, Hq, d);
   if (qs < 0 || T < 1 || !fits(T) || !fits(Hq) || !ints(table, dev, 2) || !ints(q_start, dev, 1) ||
@@ -96,12 +107,13 @@ py::object attn(const at::Tensor &buf, int64_t stream, const at::Tensor &q, cons
   return py::make_tuple(out, want_lse ? py::cast(lse) : none());
 }
 
-py::object append(const at::Tensor &buf, int64_t stream, const at::Tensor &K, const at::Tensor &V,
+py::object append(const py::object &ws, int64_t stream, const at::Tensor &K, const at::Tensor &V,
                   const at::Tensor &k_new, const at::Tensor &v_new, const at::Tensor &slots) {
   if (!caches(K, V) || k_new.scalar_type() != K.scalar_type() ||
       v_new.scalar_type() != K.scalar_type())
     return none();
   const at::Device dev = K.device();
+  const at::Tensor buf = buffer(ws);
   const int64_t T = k_new.dim() == 3 ? k_new.size(0) : 0, Hkv = K.size(1), d = K.size(3);
   const int64_t ks = row_stride(k_new, dev, Hkv, d), vs = row_stride(v_new, dev, Hkv, d);
   if (ks < 0 || vs < 0 || T < 1 || !fits(T) || v_new.size(0) != T || !ints(slots, dev, 1) ||
@@ -123,12 +135,13 @@ py::object append(const at::Tensor &buf, int64_t stream, const at::Tensor &K, co
 }
 
 // (kv_lens, q_start, positions, slots, free_left): the given ones or new ones
-py::object plan(const at::Tensor &buf, int64_t stream, const at::Tensor &new_lens,
+py::object plan(const py::object &ws, int64_t stream, const at::Tensor &new_lens,
                 const at::Tensor &lens, const at::Tensor &table, const at::Tensor &free_pages,
                 const at::Tensor &free_count, int64_t page, int64_t T, int64_t pages,
                 const c10::optional<at::Tensor> &kv_given,
                 const c10::optional<at::Tensor> &left_given) {
   const at::Device dev = new_lens.device();
+  const at::Tensor buf = buffer(ws);
   if (!dev.is_cuda() || !ints(new_lens, dev, 1) || !ints(lens, dev, 1) || !ints(table, dev, 2) ||
       !ints(free_pages, dev, 1) || !ints(free_count, dev, 1) || !fits(page) || !fits(T) ||
       !fits(pages) || buf.device() != dev)

@@ -17,7 +17,7 @@ A serving step is ``paged_plan`` once, then per layer ``paged_append`` and
     lens, free_count = p["kv_lens"], p["free_left"]
 
 Without ``ws`` a call uses a workspace kept for its device and stream, which
-host threads may share: a call's kernels are enqueued under its lock.  Inside
+host threads may share: the kernels of one call are enqueued together.  Inside
 a stream capture it takes one from the graph's own memory instead, so two
 captured graphs never share scratch.  Calls given one Workspace are ordered by
 the caller, and a capture needs it to be large enough already.  ``check``
@@ -33,7 +33,7 @@ import threading
 
 import torch
 
-from . import DTYPE_CODES, Workspace, _check, _need_result, load, read_device_status
+from . import DTYPE_CODES, Workspace, _check, _need_result, lib_path, load, read_device_status
 
 _HEADER = 4096  # workspace bytes of the calls that only report a status
 _stream_ws: dict = {}
@@ -48,8 +48,20 @@ class _PagedShape(ctypes.Structure):
 
 @functools.lru_cache(maxsize=None)
 def _entry(name: str):
-    """A C entry point of the loaded library."""
-    return getattr(load(), name)
+    """A C entry point of the loaded library, called with Python's global lock
+    held: an attention is up to three kernels over one schedule and its
+    partials, and threads that share a stream must not mix those of two calls
+    (the compiled calls hold the lock too)."""
+    load()
+    fn = getattr(_gil_library(), name)
+    like = getattr(load(), name)
+    fn.restype, fn.argtypes = like.restype, like.argtypes
+    return fn
+
+
+@functools.lru_cache(maxsize=None)
+def _gil_library():
+    return ctypes.PyDLL(lib_path())
 
 
 @functools.lru_cache(maxsize=512)
@@ -114,10 +126,9 @@ def _one_device(t, *ts) -> int:
 
 
 def _kept(dev: int, stream: int) -> Workspace:
-    """The workspace kept for a device's stream.  An attention is up to three
-    kernels over one schedule and its partials, and the C call that enqueues
-    them runs without Python's global lock, so threads that share a stream take
-    turns under the workspace's own lock, from its growth to the last launch."""
+    """The workspace kept for a device's stream.  Its lock goes from its growth
+    to the call that uses it, for threads that share the stream; the compiled
+    calls, which read ``buf`` and launch without a break, need none."""
     ws = _stream_ws.get((dev, stream))
     if ws is None:
         ws = Workspace(f"cuda:{dev}")
@@ -127,16 +138,17 @@ def _kept(dev: int, stream: int) -> Workspace:
     return ws
 
 
-def _launch(what: str, ws: Workspace | None, dev: int, nbytes: int, check: bool, call):
-    """One call on the current device and stream: call(buffer address, bytes,
-    stream) with a workspace of nbytes, then its status."""
+def _launch(what: str, args, ws: Workspace | None, dev: int, nbytes: int, check: bool):
+    """One C call sparse_<what>(*args, workspace of nbytes, stream) on the
+    current device and stream, then its status."""
+    call = _entry(f"sparse_{what}")
     stream = torch._C._cuda_getCurrentRawStream(dev)
     capturing = torch._C._cuda_isCurrentStreamCapturing()
     if ws is None and not capturing:
         ws = _kept(dev, stream)
         with ws.lock:
             buf = ws.get(nbytes)
-            rc = call(buf.data_ptr(), buf.numel(), stream)
+            rc = call(*args, buf.data_ptr(), buf.numel(), stream)
         return _finish(rc, what, ws, check)
     if capturing and check:
         raise ValueError("check=True synchronises: give check=False inside a stream capture")
@@ -145,7 +157,7 @@ def _launch(what: str, ws: Workspace | None, dev: int, nbytes: int, check: bool,
         buf = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
         if nbytes > _HEADER:
             buf[:_HEADER].zero_()
-        return _finish(call(buf.data_ptr(), nbytes, stream), what, None, check)
+        return _finish(call(*args, buf.data_ptr(), nbytes, stream), what, None, check)
     if ws.device.index not in (None, dev):
         raise ValueError(f"workspace on {ws.device}, tensors on cuda:{dev}")
     if capturing:
@@ -155,7 +167,7 @@ def _launch(what: str, ws: Workspace | None, dev: int, nbytes: int, check: bool,
         # the graph keeps this address, also when ws grows later
         ws.kept = getattr(ws, "kept", []) + [ws.buf]
     buf = ws.get(nbytes)
-    return _finish(call(buf.data_ptr(), buf.numel(), stream), what, ws, check)
+    return _finish(call(*args, buf.data_ptr(), buf.numel(), stream), what, ws, check)
 
 
 def _finish(rc: int, what: str, ws, check: bool):
@@ -217,9 +229,8 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
         plain = _plain(new_lens)
         if plain is not None:
             calls, w, stream = plain
-            with w.lock:
-                r = calls.plan(w.buf, stream, new_lens, lens, block_table, free_pages, free_count,
-                               int(page_size), int(num_tokens), int(num_pages), kv_lens, free_left)
+            r = calls.plan(w, stream, new_lens, lens, block_table, free_pages, free_count,
+                           int(page_size), int(num_tokens), int(num_pages), kv_lens, free_left)
             if type(r) is tuple:
                 _finish(0, "paged_plan", w, check)
                 return {"kv_lens": r[0], "q_start": r[1], "positions": r[2], "slots": r[3],
@@ -256,10 +267,10 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
         new = iter(torch.empty(sum(want), dtype=_I32, device=new_lens.device).split(want))
         res = [next(new) if t is None else t for t in res]
     positions, slots, kv_lens, q_start, free_left = res
-    _launch("paged_plan", ws, dev, _HEADER, check, lambda at, n, stream: _entry("sparse_paged_plan")(
+    _launch("paged_plan", (
         sh, new_lens.data_ptr(), lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), F,
         free_count.data_ptr(), kv_lens.data_ptr(), q_start.data_ptr(), positions.data_ptr(),
-        slots.data_ptr(), free_left.data_ptr(), at, n, stream))
+        slots.data_ptr(), free_left.data_ptr()), ws, dev, _HEADER, check)
     return {"kv_lens": kv_lens, "q_start": q_start, "positions": positions, "slots": slots,
             "free_left": free_left}
 
@@ -273,8 +284,7 @@ def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: 
         plain = _plain(K)
         if plain is not None:
             calls, w, stream = plain
-            with w.lock:
-                r = calls.append(w.buf, stream, K, V, k_new, v_new, slots)
+            r = calls.append(w, stream, K, V, k_new, v_new, slots)
             if r is not None:
                 return _finish(r, "paged_append", w, check)
     dev = _one_device(K, V, k_new, v_new, slots)
@@ -292,10 +302,9 @@ def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: 
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return paged_append(K, V, k_new, v_new, slots, ws, check)
-    _launch("paged_append", ws, dev, _HEADER, check,
-            lambda at, n, stream: _entry("sparse_paged_append")(
-                sh, K.data_ptr(), V.data_ptr(), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
-                slots.data_ptr(), at, n, stream))
+    _launch("paged_append", (
+        sh, K.data_ptr(), V.data_ptr(), k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+        slots.data_ptr()), ws, dev, _HEADER, check)
 
 
 def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: int = 0,
@@ -316,9 +325,8 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
         plain = _plain(q)
         if plain is not None and (max_new is None or max_new >= 1):
             calls, w, stream = plain
-            with w.lock:
-                r = calls.attn(w.buf, stream, q, K, V, block_table, q_start, kv_lens, int(window),
-                               int(sinks), int(max_new or 0), return_lse, out, lse)
+            r = calls.attn(w, stream, q, K, V, block_table, q_start, kv_lens, int(window),
+                           int(sinks), int(max_new or 0), return_lse, out, lse)
             if type(r) is tuple:
                 _finish(0, "paged_attn", w, check)
                 return r
@@ -356,8 +364,8 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
         lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
     if T == 0:
         return out, lse
-    _launch("paged_attn", ws, dev, nbytes, check, lambda at, n, stream: _entry("sparse_paged_attn")(
+    _launch("paged_attn", (
         sh, q.data_ptr(), qs, K.data_ptr(), V.data_ptr(), block_table.data_ptr(),
         q_start.data_ptr(), kv_lens.data_ptr(), window, sinks, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), at, n, stream))
+        None if lse is None else lse.data_ptr()), ws, dev, nbytes, check)
     return out, lse
