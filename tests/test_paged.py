@@ -836,3 +836,32 @@ def test_attn_from_threads_of_one_stream(lib):
     for x, g in zip(xs, got):
         _assert_attn(x, g[0])
         assert all(torch.equal(a[0], g[0][0]) and torch.equal(a[1], g[0][1]) for a in g)
+
+
+# ---- status -----------------------------------------------------------------------------
+
+def test_a_workspace_that_grows_keeps_its_status():
+    ws = sd.Workspace("cpu")
+    ws.get(4096)[:4] = torch.tensor([2, 1, 0, 0], dtype=torch.uint8)
+    ws.buf[4:64] = 7
+    grown = ws.get(4 << 20)
+    assert grown.numel() == 4 << 20 and grown[:4].tolist() == [2, 1, 0, 0]
+    assert not grown[4:].any()
+    assert ws.get(5) is grown
+
+
+@gpu
+@pytest.mark.parametrize("kept", [True, False])
+def test_errors_before_a_growing_call_are_reported(lib, kept):
+    """A batch that the plan refused, unread, then an attention that needs a
+    larger workspace."""
+    ws = None if kept else sd.Workspace()
+    sd.paged._stream_ws.clear()
+    x = _batch([300], [300], 8, 2, 128, 16, BF16)
+    table = torch.full((1, 40), -1, dtype=torch.int32, device="cuda")
+    p = sd.paged_plan(_i32([300]), _i32([0]), table, _i32([0, 1]), _i32([2]), 16, 300, 40, ws=ws,
+                      check=False)
+    q, K, V = x["args"][:3]
+    with pytest.raises(sd.SparseDecodeError, match="CAPACITY"):
+        sd.paged_attn(q, K, V, table, p["q_start"], p["kv_lens"], ws=ws)
+    sd.paged_attn(*x["args"], ws=ws)  # read, and clear again

@@ -234,7 +234,7 @@ def workspace_bytes(B, N, Hq, Hkv, d, dtype, k_or_cap: int, L: int) -> int:
 class Workspace:
     """A zero-initialised device workspace that grows on demand.  Calls that
     share one must be ordered on the same stream.  Growing replaces the
-    buffer: a CUDA graph captured earlier keeps using the old one, so whoever
+    buffer (the status word goes along): a CUDA graph captured earlier keeps using the old one, so whoever
     holds such a graph also holds a reference to the buffer it captured
     (DecodeStepGraph does)."""
 
@@ -244,9 +244,15 @@ class Workspace:
         self.buf = None
 
     def get(self, nbytes: int) -> torch.Tensor:
-        if self.buf is None or self.buf.numel() < nbytes:
+        old = self.buf
+        if old is None or old.numel() < nbytes:
             self.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8,
                                    device=self.device)
+            if old is not None and not (old.is_cuda and torch.cuda.is_current_stream_capturing()):
+                # conditions that nobody has read yet stay readable (or-ed: a
+                # call may already have found the new buffer; not in a graph,
+                # whose replays would read the old buffer after its end)
+                self.buf[:4].bitwise_or_(old[:4])
         return self.buf
 
 
