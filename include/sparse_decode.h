@@ -450,6 +450,23 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
                                   const int32_t *kv_lens, int32_t window, int32_t sinks, void *out,
                                   float *lse, void *ws, size_t ws_bytes, void *stream);
 
+/* sparse_paged_attn with its device conditions or-ed into *status (a device
+ * word, 4-byte aligned) instead of the first word of ws: for a workspace that
+ * nobody can read later, such as a captured graph's own memory. */
+sparse_status_t sparse_paged_attn_status(const sparse_paged_shape_t *shape, const void *q,
+                                         int64_t q_stride, const void *K, const void *V,
+                                         const int32_t *block_table, const int32_t *q_start,
+                                         const int32_t *kv_lens, int32_t window, int32_t sinks,
+                                         void *out, float *lse, void *ws, size_t ws_bytes,
+                                         uint32_t *status, void *stream);
+
+/* *ws = a status area of the library's own on the current device, 4096 bytes
+ * that start at zero and last as long as the library is loaded: a workspace
+ * for the paged calls that need no more (plan, append), and the status word of
+ * sparse_paged_attn_status.  Calls that share it may overlap.  Read it with
+ * sparse_read_device_status.  Synchronous; allowed while a stream captures. */
+sparse_status_t sparse_paged_static_status(void **ws);
+
 /* Self-test of failure detection, with no fault: one device thread waits,
  * through the bounded wait that every counter barrier of the library uses
  * (the Louver query's per-head barrier), on a workspace word that nothing

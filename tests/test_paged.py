@@ -94,6 +94,17 @@ def test_paged_calls_refuse_bad_pointers_and_sizes(lib):
     assert attn(nb=4096) == 3
 
 
+def test_status_elsewhere_is_refused_like_the_rest(lib):
+    sh, F = _pshape(), 1 << 20
+    p = lambda x: ctypes.c_void_p(x)
+    def attn(status, ws=F, nb=1 << 32):
+        return lib.sparse_paged_attn_status(ctypes.byref(sh), p(F), 512, p(F << 1), p(F << 2),
+                                            p(F), p(F), p(F), 0, 0, p(F << 3), None, p(ws), nb,
+                                            p(status), None)
+    assert attn(None) == 1 and attn(F + 2) == 1 and attn(F, ws=None) == 1 and attn(F, nb=16) == 3
+    assert lib.sparse_paged_static_status(None) == 1
+
+
 @pytest.mark.parametrize("T,stride", [(1, 512), (3, 512), (3, 1024)])
 def test_attn_refuses_results_over_its_inputs(lib, T, stride):
     """Also where only the first or the last 16 bytes are shared."""
@@ -865,3 +876,44 @@ def test_errors_before_a_growing_call_are_reported(lib, kept):
     with pytest.raises(sd.SparseDecodeError, match="CAPACITY"):
         sd.paged_attn(q, K, V, table, p["q_start"], p["kv_lens"], ws=ws)
     sd.paged_attn(*x["args"], ws=ws)  # read, and clear again
+
+
+@gpu
+@pytest.mark.parametrize("new", [1, 40])
+def test_errors_of_a_replayed_graph_are_reported(lib, new):
+    """A captured step without a workspace whose replays run out of pages, then
+    one whose block table goes bad."""
+    Hq, Hkv, d, page, pages = 8, 2, 64, 16, 12
+    K = torch.zeros(pages, Hkv, page, d, dtype=BF16, device="cuda")
+    V = torch.zeros_like(K)
+    free = torch.arange(3, pages, dtype=torch.int32, device="cuda")
+    table, count, lens, n = _i32([[0, 1, 2] + [-1] * 13]), _i32([1]), _i32([40]), _i32([new])
+    q = torch.zeros(new, Hq, d, dtype=BF16, device="cuda")
+    k = torch.zeros(new, Hkv, d, dtype=BF16, device="cuda")
+    sd.paged_status(raise_on_error=False)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        p = sd.paged_plan(n, lens, table, free, count, page, new, pages, check=False,
+                          kv_lens=lens, free_left=count)
+        sd.paged_append(K, V, k, k, p["slots"], check=False)
+        sd.paged_attn(q, K, V, table, p["q_start"], lens, max_new=new, check=False)
+    assert sd.paged_status() == 0
+    for _ in range(40):
+        gr.replay()
+    with pytest.raises(sd.SparseDecodeError, match="CAPACITY"):
+        sd.paged_status()
+    assert sd.paged_status() == 0
+    table[0, 0] = pages
+    lens.fill_(20), count.fill_(9)
+    gr.replay()
+    assert sd.paged_status(raise_on_error=False) == 8  # INDEX: the attention's
+
+
+@gpu
+def test_status_of_unchecked_calls(lib):
+    table = torch.full((1, 4), -1, dtype=torch.int32, device="cuda")
+    sd.paged_status(raise_on_error=False)
+    sd.paged_plan(_i32([60]), _i32([10]), table, _i32([0]), _i32([1]), 16, 60, 8, check=False)
+    with pytest.raises(sd.SparseDecodeError, match="CAPACITY"):
+        sd.paged_status()
+    assert sd.paged_status() == 0

@@ -30,7 +30,7 @@ __all__ = ["SparseDecodeError", "lib_path", "load", "score", "select_topk",
            "kv_append", "LouverIndex", "louver_build", "louver_route_threshold",
            "DecodeStepGraph", "selftest_bounded_wait", "louver_decode_step",
            "device_usable", "read_device_flags", "FLAG_SLOW_SELECT",
-           "paged_plan", "paged_append", "paged_attn", "paged_workspace_bytes"]
+           "paged_plan", "paged_append", "paged_attn", "paged_workspace_bytes", "paged_status"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_FILE = os.path.join(_PKG, "libsparse_decode.so")
@@ -53,6 +53,7 @@ EXPORTED_SYMBOLS = (
     "sparse_pointer_device_usable", "sparse_graph_launch", "sparse_decode_step_join",
     "sparse_decode_step_fused", "sparse_graph_upload", "sparse_paged_workspace_size",
     "sparse_paged_plan", "sparse_paged_append", "sparse_paged_attn",
+    "sparse_paged_attn_status", "sparse_paged_static_status",
 )
 
 DTYPE_CODES = {torch.float32: 0, torch.bfloat16: 1}
@@ -129,6 +130,9 @@ def load():
             "sparse_paged_plan": (I32, [P, P, P, P, P, I32, P, P, P, P, P, P, P, SZ, P]),
             "sparse_paged_append": (I32, [P, P, P, P, I64, P, I64, P, P, SZ, P]),
             "sparse_paged_attn": (I32, [P, P, I64, P, P, P, P, P, I32, I32, P, P, P, SZ, P]),
+            "sparse_paged_attn_status": (I32, [P, P, I64, P, P, P, P, P, I32, I32, P, P, P, SZ, P,
+                                               P]),
+            "sparse_paged_static_status": (I32, [ctypes.POINTER(P)]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -974,4 +978,5 @@ def louver_decode_step(q_route, q_layers, K, V, index: LouverIndex, tau, cap: in
     return {"idx": idx, "count": count, "out": out, "lse": lse}
 
 
-from .paged import paged_append, paged_attn, paged_plan, paged_workspace_bytes  # noqa: E402
+from .paged import (paged_append, paged_attn, paged_plan, paged_status,  # noqa: E402
+                    paged_workspace_bytes)

@@ -66,6 +66,9 @@ PagedLayout layout(const PagedShape &s) {
   return l;
 }
 
+// the status area of calls whose workspaces are temporaries
+__device__ __align__(256) unsigned char g_static_status[kPagedHeader];
+
 sparse_status_t status_of(cudaError_t e) {
   return e == cudaSuccess ? SPARSE_OK : SPARSE_ERR_CUDA;
 }
@@ -144,6 +147,17 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
                                   const int32_t *block_table, const int32_t *q_start,
                                   const int32_t *kv_lens, int32_t window, int32_t sinks, void *out,
                                   float *lse, void *ws, size_t ws_bytes, void *stream) {
+  return sparse_paged_attn_status(shape, q, q_stride, K, V, block_table, q_start, kv_lens, window,
+                                  sinks, out, lse, ws, ws_bytes, static_cast<uint32_t *>(ws),
+                                  stream);
+}
+
+sparse_status_t sparse_paged_attn_status(const sparse_paged_shape_t *shape, const void *q,
+                                         int64_t q_stride, const void *K, const void *V,
+                                         const int32_t *block_table, const int32_t *q_start,
+                                         const int32_t *kv_lens, int32_t window, int32_t sinks,
+                                         void *out, float *lse, void *ws, size_t ws_bytes,
+                                         uint32_t *status, void *stream) {
   PagedShape s;
   sparse_status_t r = sd::check_paged(shape, &s);
   if (r != SPARSE_OK) return r;
@@ -157,7 +171,8 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
   for (const void *p : {(const void *)block_table, (const void *)q_start, (const void *)kv_lens,
                         (const void *)lse})
     if (!sd::aligned(p, 4)) return SPARSE_ERR_INVALID_ARG;
-  if (!ws || !sd::aligned(ws, 256)) return SPARSE_ERR_INVALID_ARG;
+  if (!ws || !sd::aligned(ws, 256) || !status || !sd::aligned(status, 4))
+    return SPARSE_ERR_INVALID_ARG;
   const sd::PagedLayout l = sd::layout(s);
   if (ws_bytes < l.total) return SPARSE_ERR_WORKSPACE;
   // results written while other blocks still read: never over the inputs
@@ -196,7 +211,7 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
   a.sinks = window > 0 ? sinks : 0;  // without a window every earlier key is seen
   a.max_new = s.max_new;
   a.scale_log2 = (float)(1.4426950408889634 / (s.d == 64 ? 8.0 : 11.313708498984761));
-  a.status = reinterpret_cast<uint32_t *>(w);
+  a.status = status;
   a.head = reinterpret_cast<sd::PgHead *>(w + l.head_off);
   a.seqs = reinterpret_cast<sd::PgSeq *>(w + l.seqs_off);
   a.runs = reinterpret_cast<uint32_t *>(w + sd::kRunsOff);
@@ -212,6 +227,17 @@ sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void 
     return sd::status_of(few ? sd::launch_paged_decode_f32(s, a, st)
                              : sd::launch_paged_chunk_f32(s, a, st));
   return sd::status_of(few ? sd::launch_paged_decode(s, a, st) : sd::launch_paged_chunk(s, a, st));
+}
+
+sparse_status_t sparse_paged_static_status(void **ws) {
+  if (!ws) return SPARSE_ERR_INVALID_ARG;
+  // the lookup may load the library's code: allowed while this thread captures
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return SPARSE_ERR_CUDA;
+  e = cudaGetSymbolAddress(ws, sd::g_static_status);
+  const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+  return sd::status_of(e == cudaSuccess ? back : e);
 }
 
 }  // extern "C"

@@ -19,9 +19,12 @@ A serving step is ``paged_plan`` once, then per layer ``paged_append`` and
 Without ``ws`` a call uses a workspace kept for its device and stream, which
 host threads may share: the kernels of one call are enqueued together.  Inside
 a stream capture it takes one from the graph's own memory instead, so two
-captured graphs never share scratch.  Calls given one Workspace are ordered by
-the caller, and a capture needs it to be large enough already.  ``check``
-reads the device status (and synchronises); a capture needs check=False.
+captured graphs share scratch only if they share a memory pool, and then they
+must not overlap.  Calls given one Workspace are ordered by the caller, and a
+capture needs it to be large enough already.  ``check`` reads the device status
+(and synchronises); a capture needs check=False.  What calls with check=False
+and the replays of a graph report is read later, with ``paged_status`` where
+they had no ``ws``, else with ``read_device_status(ws)``.
 """
 from __future__ import annotations
 
@@ -153,11 +156,14 @@ def _launch(what: str, args, ws: Workspace | None, dev: int, nbytes: int, check:
     if capturing and check:
         raise ValueError("check=True synchronises: give check=False inside a stream capture")
     if ws is None:
+        status = _static_status(dev)
+        if nbytes <= _HEADER:
+            return _finish(call(*args, status, _HEADER, stream), what, None, check)
         # only the header has to start at zero: the graph clears it
         buf = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-        if nbytes > _HEADER:
-            buf[:_HEADER].zero_()
-        return _finish(call(*args, buf.data_ptr(), nbytes, stream), what, None, check)
+        buf[:_HEADER].zero_()
+        return _finish(_entry(f"sparse_{what}_status")(*args, buf.data_ptr(), nbytes, status,
+                                                       stream), what, None, check)
     if ws.device.index not in (None, dev):
         raise ValueError(f"workspace on {ws.device}, tensors on cuda:{dev}")
     if capturing:
@@ -175,6 +181,33 @@ def _finish(rc: int, what: str, ws, check: bool):
         _check(rc, what)
     if check:
         read_device_status(ws)
+
+
+@functools.lru_cache(maxsize=None)
+def _static_status(dev: int) -> int:
+    """The address of the library's status area on the current device: a
+    captured call without ``ws`` reports there, since its scratch is the graph's."""
+    at = ctypes.c_void_p(0)
+    _check(_entry("sparse_paged_static_status")(ctypes.byref(at)), "paged status")
+    return at.value
+
+
+def paged_status(raise_on_error: bool = True) -> int:
+    """Synchronise the current stream and read (and reset) the device status of
+    the paged calls made without ``ws``: those on this stream, and those that
+    any graph captured on this device has replayed up to now.  Raises
+    SparseDecodeError unless it is SPARSE_OK; else returns it."""
+    dev = torch.cuda.current_device()
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    ws = _stream_ws.get((dev, stream))
+    rc, seen = 0, 0
+    for at in ([] if ws is None else [ws.buf.data_ptr()]) + [_static_status(dev)]:
+        flags = ctypes.c_uint32(0)
+        rc = load().sparse_read_device_status(at, stream, ctypes.byref(flags)) or rc
+        seen |= flags.value
+    if raise_on_error:
+        _check(rc, f"device status (flags=0x{seen:x})")
+    return rc
 
 
 def _rows(t, name: str, heads: int, d: int) -> int:
