@@ -917,3 +917,48 @@ def test_status_of_unchecked_calls(lib):
     with pytest.raises(sd.SparseDecodeError, match="CAPACITY"):
         sd.paged_status()
     assert sd.paged_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("checked", [True, False])
+def test_a_wait_that_ran_out_costs_the_kept_workspace(lib, checked):
+    x = _batch([1], [300], 8, 2, 64, 16, BF16)
+    sd.paged_attn(*x["args"], max_new=1)
+    stream = torch.cuda.current_stream().cuda_stream
+    ws = sd.paged._stream_ws[torch.cuda.current_device(), stream]
+    # a word that nothing increments, given up after a millisecond
+    assert lib.sparse_selftest_bounded_wait(ws.buf.data_ptr(), ws.buf.numel(), 1000000,
+                                            stream) == 0
+    with pytest.raises(sd.SparseDecodeError, match="TIMEOUT"):
+        sd.paged_attn(*x["args"], max_new=1) if checked else sd.paged_status()
+    assert ws not in sd.paged._stream_ws.values()
+    _assert_attn(x, sd.paged_attn(*x["args"], max_new=1))
+    assert sd.paged._stream_ws[torch.cuda.current_device(), stream] is not ws
+
+
+@gpu
+def test_kept_workspaces_can_be_freed(lib):
+    x = _batch([300], [300], 8, 2, 128, 16, BF16)
+    sd.paged_release()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    got = sd.paged_attn(*x["args"])
+    del got
+    assert torch.cuda.memory_allocated() > before + (1 << 20)
+    sd.paged_release()
+    assert torch.cuda.memory_allocated() == before
+    _assert_attn(x, sd.paged_attn(*x["args"]))
+
+
+def test_only_a_wait_that_ran_out_costs_the_kept_workspace(monkeypatch):
+    from token_sparse_attention_sm_b200 import paged
+    monkeypatch.setattr(paged, "_stream_ws", {})
+    kept, own = sd.Workspace("cpu"), sd.Workspace("cpu")
+    kept.key = (0, 0)
+    for ws, status, left in ((kept, 8, 1), (own, 7, 1), (None, 7, 1), (kept, 7, 0)):
+        paged._stream_ws[0, 0] = kept
+        paged._drop_after(status, ws)
+        assert len(paged._stream_ws) == left
+    paged._stream_ws[0, 0] = kept
+    sd.paged_release()
+    assert not paged._stream_ws

@@ -30,7 +30,8 @@ __all__ = ["SparseDecodeError", "lib_path", "load", "score", "select_topk",
            "kv_append", "LouverIndex", "louver_build", "louver_route_threshold",
            "DecodeStepGraph", "selftest_bounded_wait", "louver_decode_step",
            "device_usable", "read_device_flags", "FLAG_SLOW_SELECT",
-           "paged_plan", "paged_append", "paged_attn", "paged_workspace_bytes", "paged_status"]
+           "paged_plan", "paged_append", "paged_attn", "paged_workspace_bytes", "paged_status",
+           "paged_release"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_FILE = os.path.join(_PKG, "libsparse_decode.so")
@@ -978,5 +979,5 @@ def louver_decode_step(q_route, q_layers, K, V, index: LouverIndex, tau, cap: in
     return {"idx": idx, "count": count, "out": out, "lse": lse}
 
 
-from .paged import (paged_append, paged_attn, paged_plan, paged_status,  # noqa: E402
-                    paged_workspace_bytes)
+from .paged import (paged_append, paged_attn, paged_plan, paged_release,  # noqa: E402
+                    paged_status, paged_workspace_bytes)

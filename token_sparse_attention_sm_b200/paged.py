@@ -36,9 +36,11 @@ import threading
 
 import torch
 
-from . import DTYPE_CODES, Workspace, _check, _need_result, lib_path, load, read_device_status
+from . import (DTYPE_CODES, SparseDecodeError, Workspace, _check, _need_result, lib_path, load,
+               read_device_status)
 
 _HEADER = 4096  # workspace bytes of the calls that only report a status
+_TIMEOUT = 7  # SPARSE_ERR_TIMEOUT
 _stream_ws: dict = {}
 _I32, _F32 = torch.int32, torch.float32
 
@@ -135,7 +137,7 @@ def _kept(dev: int, stream: int) -> Workspace:
     ws = _stream_ws.get((dev, stream))
     if ws is None:
         ws = Workspace(f"cuda:{dev}")
-        ws.lock = threading.RLock()
+        ws.lock, ws.key = threading.RLock(), (dev, stream)
         ws.get(_HEADER)  # whoever finds it finds a buffer
         ws = _stream_ws.setdefault((dev, stream), ws)
     return ws
@@ -180,7 +182,19 @@ def _finish(rc: int, what: str, ws, check: bool):
     if rc:
         _check(rc, what)
     if check:
-        read_device_status(ws)
+        try:
+            read_device_status(ws)
+        except SparseDecodeError as e:
+            _drop_after(e.status, ws)
+            raise
+
+
+def _drop_after(status: int, ws: Workspace | None):
+    """A wait that ran out leaves counters that are not zero: the next call
+    without ``ws`` gets a new workspace."""
+    key = getattr(ws, "key", None)  # None: not a kept one
+    if status == _TIMEOUT and key is not None and _stream_ws.get(key) is ws:
+        del _stream_ws[key]
 
 
 @functools.lru_cache(maxsize=None)
@@ -205,9 +219,17 @@ def paged_status(raise_on_error: bool = True) -> int:
         flags = ctypes.c_uint32(0)
         rc = load().sparse_read_device_status(at, stream, ctypes.byref(flags)) or rc
         seen |= flags.value
+    _drop_after(rc, ws)
     if raise_on_error:
         _check(rc, f"device status (flags=0x{seen:x})")
     return rc
+
+
+def paged_release() -> None:
+    """Free the workspaces kept for the paged calls without ``ws`` (one per
+    device and stream, up to 80 MB once it has served a large chunk).  Later
+    calls make new ones; conditions that nobody has read are dropped."""
+    _stream_ws.clear()
 
 
 def _rows(t, name: str, heads: int, d: int) -> int:
