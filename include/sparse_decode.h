@@ -441,9 +441,13 @@ sparse_status_t sparse_paged_append(const sparse_paged_shape_t *shape, void *K, 
  * SPARSE_ERR_INDEX; a sequence with lengths outside the shape (rows outside
  * [0,T], more than max_new new tokens, a negative kv_len or one beyond its
  * table row) is skipped and raises it too.  Rows of K and V that no new token
- * of the sequence sees are never used, whatever they hold; one that some new
- * tokens see must be finite (a value times a weight of zero reaches the
- * tokens near them that do not see it). */
+ * of the sequence sees are never used, whatever they hold.  A row of V that
+ * some new tokens see must be finite (a value times a weight of zero reaches
+ * the tokens near them that do not see it).  A row of out whose scores hold a
+ * NaN or +inf (from q or a visible row of K) is NaN, and so is its lse; the
+ * other rows are not touched by it.  (In fp32 with more than 16 rows per KV
+ * head, max_new * Hq / Hkv, an infinite element of q or K makes every score it
+ * enters NaN.) */
 sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void *q,
                                   int64_t q_stride, const void *K, const void *V,
                                   const int32_t *block_table, const int32_t *q_start,

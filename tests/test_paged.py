@@ -962,3 +962,43 @@ def test_only_a_wait_that_ran_out_costs_the_kept_workspace(monkeypatch):
     paged._stream_ws[0, 0] = kept
     sd.paged_release()
     assert not paged._stream_ws
+
+
+# ---- values that are not finite -----------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,kv", [([1, 1], [700, 90]), ([1, 1], [20000, 90]),
+                                    ([3, 2], [700, 90]), ([40, 7], [700, 90]),
+                                    ([40, 1], [9000, 90]), ([300, 1], [300, 90])])
+@pytest.mark.parametrize("what", ["key nan", "key inf", "query nan", "query inf"])
+@pytest.mark.parametrize("window", [0, 30])
+def test_attn_scores_that_are_not_finite(lib, dtype, d, new, kv, what, window):
+    """A row with a score that is NaN or +inf has no softmax: out and lse are
+    NaN, and lse is not the -inf of a row that sees nothing.  Rows that do not
+    see the key, the other heads and the other sequence are as ever."""
+    Hq, Hkv = 8, 2
+    x = _batch(new, kv, Hq, Hkv, d, 16, dtype, seed=d)
+    q, K, V, table = x["args"][:4]
+    n, c = new[0], kv[0]
+    value = float("nan") if what.endswith("nan") else float("inf")
+    j = c - min(n, 2)       # the last or the last but one new token
+    p = torch.arange(c - n, c)
+    bad = torch.zeros(sum(new), Hq, dtype=torch.bool)
+    sees = (p >= j) & ((p - window < j) if window else torch.ones_like(p, dtype=torch.bool))
+    if what.startswith("key"):
+        q[:n, 4:, 3] = q[:n, 4:, 3].abs() + 0.5     # of KV head 1
+        x["q"][:n, 4:, 3] = x["q"][:n, 4:, 3].abs() + 0.5
+        K[table[0, j // 16], 1, j % 16, 3] = value
+        bad[:n, 4:] = sees[:, None]
+    else:
+        q[n - 1, 2, 5] = value
+        bad[n - 1, 2] = True
+    out, lse, tol, ltol = _definition(x, window, 0)
+    got_out, got_lse = (t.double().cpu() for t in
+                        sd.paged_attn(*x["args"], window=window, max_new=max(new)))
+    assert torch.equal(torch.isnan(got_lse), bad)
+    assert torch.equal(torch.isnan(got_out).all(-1), bad) and not torch.isnan(got_out[~bad]).any()
+    assert ((got_out - out).abs() / tol)[~bad].max() <= 1
+    assert ((got_lse - lse).abs() / ltol)[~bad].max() <= 1

@@ -109,6 +109,14 @@ __device__ __forceinline__ float pg_exp2(float x) {
   return y;
 }
 
+// What a row's sum of weights l makes of its O, and its lse (m: its reference
+// in log2 units).  l is 0 when the row sees nothing; a score that is NaN or
+// +inf leaves l NaN, and that stays in both.
+__device__ __forceinline__ float pg_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float pg_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
 // The key tiles a block of tokens [t0, t1) of a sequence reads: tiles
 // [0, sink_tiles) and [lo, hi), KT keys each.
 struct PgTiles {
@@ -237,13 +245,12 @@ __device__ __forceinline__ void pg_merge(const PgArgs &a, size_t slot0, int np, 
       if (i >= total) break;
       const size_t o = at(row0 + i / (D / 4));
       const int c = i % (D / 4);
-      const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
+      const float inv = pg_inverse(l[e]);
       alignas(16) T r[4] = {DT<T>::from_f(acc[e].x * inv), DT<T>::from_f(acc[e].y * inv),
                 DT<T>::from_f(acc[e].z * inv), DT<T>::from_f(acc[e].w * inv)};
       using Vec = typename std::conditional<sizeof(T) == 4, float4, uint2>::type;
       *reinterpret_cast<Vec *>(out + o * D + c * 4) = *reinterpret_cast<const Vec *>(r);
-      if (a.lse && c == 0)
-        a.lse[o] = l[e] > 0.f ? (m[e] + log2f(l[e])) * 0.69314718055994531f : -INFINITY;
+      if (a.lse && c == 0) a.lse[o] = pg_lse(m[e], l[e]);
     }
   }
 }

@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         ch_fence_after();
       }
       const size_t at = (size_t)(I.row0 + I.t0 + a.by_G(br)) * a.Hq + I.h * G + br - a.by_G(br) * G;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = pg_inverse(l);
       const size_t per = (size_t)a.part_rows * D;
       const size_t mine = (size_t)I.slot * a.Hkv + I.h;
       float2 *ml = reinterpret_cast<float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
@@ -738,8 +738,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       __syncwarp();
       if (lane == 0 && n > 0) mbar_arrive(&sm->o_empty[t]);
       if (I.np == 1) {
-        if (live && a.lse)
-          a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (live && a.lse) a.lse[at] = pg_lse(m, l);
         done();
         continue;
       }

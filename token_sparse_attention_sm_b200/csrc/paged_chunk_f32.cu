@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
       const int r = warp * 16 + g8 + 8 * i;
       if (r >= rows) continue;
       const bool whole = sq.np == 1;
-      const float f = !whole ? 1.f : l[i] > 0.f ? 1.f / l[i] : 0.f;
+      const float f = whole ? pg_inverse(l[i]) : 1.f;
       float *dst = whole ? out + place(r) * D : a.part + mine * per + (size_t)r * D;
 #pragma unroll
       for (int cb = 0; cb < D / 32; ++cb)
@@ -307,8 +307,7 @@ __global__ void __launch_bounds__(kCfThreads, 1)
                           o[cb * 4 + 2][2 * i + e] * f, o[cb * 4 + 3][2 * i + e] * f);
       if (t4 == 0) {
         if (!whole) ml[mine * a.part_rows + r] = make_float2(m[i], l[i]);
-        else if (a.lse)
-          a.lse[place(r)] = l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+        else if (a.lse) a.lse[place(r)] = pg_lse(m[i], l[i]);
       }
     }
     __syncthreads();

@@ -377,11 +377,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     float2 *pml = reinterpret_cast<float2 *>(a.part + (size_t)a.slot_cap * a.Hkv * per);
     const size_t slot = 2 * (size_t)blockIdx.x + (seg.u0 == 0 ? 1 : 0);
     auto store = [&](int r, int c, float4 acc, float mm, float ll) {
-      const float inv = ll > 0.f ? 1.f / ll : 0.f;
+      const float inv = pg_inverse(ll);
       const size_t at = (size_t)(seg.row0 + a.by_G(r)) * a.Hq + seg.h * G + r - a.by_G(r) * G;
       pg_store4(out + at * D + c * 4, acc, inv);
-      if (a.lse && c == 0)
-        a.lse[at] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+      if (a.lse && c == 0) a.lse[at] = pg_lse(mm, ll);
     };
     for (int i = tid; i < rows * (D / 4); i += 32 * C::kWarps) {
       const int r = i / (D / 4), c = i % (D / 4);
