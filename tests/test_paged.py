@@ -138,6 +138,21 @@ def test_paged_python_refuses_host_tensors():
         sd.paged_plan(i, i, i[None], i, i, 16, 1, 4)
 
 
+BIG = 1 << 32
+
+
+@pytest.mark.parametrize("kw", [dict(page_size=BIG + 16), dict(num_pages=BIG + 10),
+                                dict(max_blocks=BIG + 4), dict(max_new=BIG + 1), dict(T=BIG + 8),
+                                dict(B=BIG + 2), dict(d=BIG + 64), dict(page_size=16 - BIG),
+                                dict(T=1 << 31)], ids=str)
+def test_sizes_past_32_bits_are_refused(lib, kw):
+    a = dict(B=2, T=8, Hq=8, Hkv=2, d=64, dtype=BF16, page_size=16, num_pages=10, max_blocks=4,
+             max_new=8)
+    assert sd.paged_workspace_bytes(**a) > 4096
+    with pytest.raises((ValueError, sd.SparseDecodeError)):
+        sd.paged_workspace_bytes(**{**a, **kw})
+
+
 # ---- inputs and the plain forms ------------------------------------------------------
 
 def _i32(x):
@@ -1002,3 +1017,19 @@ def test_attn_scores_that_are_not_finite(lib, dtype, d, new, kv, what, window):
     assert torch.equal(torch.isnan(got_out).all(-1), bad) and not torch.isnan(got_out[~bad]).any()
     assert ((got_out - out).abs() / tol)[~bad].max() <= 1
     assert ((got_lse - lse).abs() / ltol)[~bad].max() <= 1
+
+
+@gpu
+def test_calls_refuse_sizes_past_32_bits(lib):
+    x = _batch([2], [20], 8, 2, 64, 16, BF16)
+    q, K, V, table, qs, kv = x["args"]
+    sd.paged_attn(*x["args"])  # the stream has a workspace: the compiled calls are asked first
+    for bad in (lambda: sd.paged_plan(kv, kv, table, kv, kv, BIG + 16, 1, 4),
+                lambda: sd.paged_plan(kv, kv, table, kv, kv, 16, BIG + 1, 4),
+                lambda: sd.paged_plan(kv, kv, table, kv, kv, 16, 1, BIG + 4),
+                lambda: sd.paged_plan(kv, kv, table, kv, kv, 16, (1 << 31) - 1, 4),
+                lambda: sd.paged_attn(q, K, V, table, qs, kv, max_new=BIG + 1),
+                lambda: sd.paged_attn(q, K, V, table, qs, kv, window=BIG + 1),
+                lambda: sd.paged_attn(q, K, V, table, qs, kv, window=5, sinks=BIG)):
+        with pytest.raises((ValueError, sd.SparseDecodeError)):
+            bad()

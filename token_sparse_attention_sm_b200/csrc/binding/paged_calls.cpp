@@ -154,6 +154,8 @@ py::object plan(const py::object &ws, int64_t stream, const at::Tensor &new_lens
   if (left_given && (!ints(*left_given, dev, 1) || left_given->size(0) != 1)) return none();
   const sparse_paged_shape_t sh = {(int32_t)B,    (int32_t)T,     1, 1, 64, 0, (int32_t)page,
                                    (int32_t)pages, (int32_t)table.size(1), 0};
+  size_t need = 0;
+  if (g_size(&sh, &need) != SPARSE_OK) return none();  // nothing is allocated for it
   // one allocation: positions, slots, q_start, then what was not given; the
   // results are tensors of their own on its storage (a view op costs 0.6 us)
   const int64_t n_kv = kv_given ? 0 : B, n_left = left_given ? 0 : 1;

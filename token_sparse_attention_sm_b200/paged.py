@@ -74,8 +74,11 @@ def _shape(B, T, Hq, Hkv, d, dtype, page_size, num_pages, max_blocks, max_new=0)
     """The C shape of these sizes, by reference (read only by the library)."""
     if dtype not in DTYPE_CODES:
         raise TypeError(f"unsupported dtype {dtype}")
-    return ctypes.byref(_PagedShape(B, T, Hq, Hkv, d, DTYPE_CODES[dtype], page_size, num_pages,
-                                    max_blocks, max_new))
+    sizes = (B, T, Hq, Hkv, d, DTYPE_CODES[dtype], page_size, num_pages, max_blocks, max_new)
+    # ctypes would cut them to 32 bits without a word
+    if not all(-1 << 31 <= x < 1 << 31 for x in sizes):
+        raise ValueError("sizes must fit 32 bits")
+    return ctypes.byref(_PagedShape(*sizes))
 
 
 @functools.lru_cache(maxsize=512)
@@ -311,6 +314,9 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
         if t is not None:
             _need_int32(t, (n,), name)
     sh = _shape(B, T, 1, 1, 64, _F32, int(page_size), int(num_pages), blocks)
+    # before the results are allocated
+    _check(_entry("sparse_paged_workspace_size")(sh, ctypes.byref(ctypes.c_size_t(0))),
+           "paged_plan")
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size,
