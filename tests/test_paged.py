@@ -1033,3 +1033,42 @@ def test_calls_refuse_sizes_past_32_bits(lib):
                 lambda: sd.paged_attn(q, K, V, table, qs, kv, window=5, sinks=BIG)):
         with pytest.raises((ValueError, sd.SparseDecodeError)):
             bad()
+
+
+# ---- the build of the compiled calls ---------------------------------------------------------
+
+def test_compiled_calls_are_rebuilt_for_another_torch(monkeypatch, tmp_path, lib):
+    """The module is compiled against torch and CPython: one that was built for
+    others is not taken, however new the file."""
+    from token_sparse_attention_sm_b200 import build, paged
+    assert build.calls_current()
+    ran = []
+    def fake(cmd):
+        ran.append(cmd)
+        tag = next(c for c in cmd if c.startswith("-DPAGED_CALLS_TAG="))
+        with open(cmd[-1], "wb") as f:
+            f.write(b"x" + tag.split("=", 1)[1].strip('"').encode())
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "calls.so"))
+    monkeypatch.setattr(build.subprocess, "check_call", fake)
+    build.build_calls()
+    assert len(ran) == 1 and build.calls_current()
+    build.build_calls()
+    assert len(ran) == 1
+    monkeypatch.setattr(torch, "__version__", "2.99.0")
+    assert not build.calls_current()
+    paged._calls.cache_clear()
+    with pytest.raises(RuntimeError, match="another torch"):
+        paged._calls()
+    build.build_calls()
+    assert len(ran) == 2 and build.calls_current()
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda n: "cpython-399")
+    build.build_calls()
+    assert len(ran) == 3
+
+
+def test_the_library_is_built_before_the_compiled_calls(monkeypatch):
+    from token_sparse_attention_sm_b200 import build
+    order = []
+    monkeypatch.setattr(build, "build_library", lambda *a: order.append("library"))
+    monkeypatch.setattr(build, "build_calls", lambda *a: order.append("calls"))
+    assert build.build() == build.LIB and order == ["library", "calls"]

@@ -8,6 +8,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,15 +37,29 @@ def _newest_input():
     return max(os.path.getmtime(f) for f in files)
 
 
+def calls_tag() -> str:
+    """What _paged_calls.so is compiled against, a text that the file holds:
+    torch's version and C++ ABI, and the interpreter's ABI."""
+    import torch
+    return (f"paged_calls for torch {torch.__version__} "
+            f"abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')};")
+
+
+def calls_current() -> bool:
+    """Whether _paged_calls.so is there and fits this torch and interpreter."""
+    if not os.path.exists(CALLS):
+        return False
+    with open(CALLS, "rb") as f:
+        return calls_tag().encode() in f.read()
+
+
 def build_calls(force: bool = False) -> str:
     """_paged_calls.so: torch tensors in, the C entry points (given to it by
     address) called directly."""
     newest = max(os.path.getmtime(f) for f in
                  (CALLS_SRC, os.path.join(INCLUDE, "sparse_decode.h"), os.path.abspath(__file__)))
-    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+    if not force and calls_current() and os.path.getmtime(CALLS) >= newest:
         return CALLS
-    import sysconfig
-
     import torch
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"),
@@ -54,7 +69,7 @@ def build_calls(force: bool = False) -> str:
     subprocess.check_call([
         os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-        "-DTORCH_EXTENSION_NAME=_paged_calls", *(f"-I{p}" for p in inc), CALLS_SRC,
+        "-DTORCH_EXTENSION_NAME=_paged_calls", f'-DPAGED_CALLS_TAG="{calls_tag()}"', *(f"-I{p}" for p in inc), CALLS_SRC,
         f"-L{os.path.join(root, 'lib')}", "-lc10", "-ltorch_cpu", "-ltorch", "-ltorch_python",
         "-o", tmp])
     os.replace(tmp, CALLS)
@@ -62,7 +77,12 @@ def build_calls(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_library(force, verbose)  # needs nothing of torch
     build_calls(force)
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)

@@ -192,6 +192,7 @@ void bind(int64_t size, int64_t plan_fn, int64_t append_fn, int64_t attn_fn) {
 }  // namespace
 
 PYBIND11_MODULE(_paged_calls, m) {
+  m.attr("built_for") = PAGED_CALLS_TAG;  // read from the file before it is loaded
   m.def("bind", &bind);
   m.def("plan", &plan);
   m.def("append", &append);

@@ -31,7 +31,6 @@ from __future__ import annotations
 import ctypes
 import functools
 import importlib.util
-import os
 import threading
 
 import torch
@@ -94,11 +93,11 @@ def _attn_plan(*sizes):
 def _calls():
     """The compiled form of the calls (csrc/binding/paged_calls.cpp), given the
     library's entry points."""
-    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_paged_calls.so")
-    if not os.path.exists(path):
-        raise RuntimeError(f"not built: {path} is missing "
-                           "(run `python -m token_sparse_attention_sm_b200.build`)")
-    spec = importlib.util.spec_from_file_location("_paged_calls", path)
+    from .build import CALLS, calls_current
+    if not calls_current():
+        raise RuntimeError(f"not built: {CALLS} is missing or was built for another torch or "
+                           "Python (run `python -m token_sparse_attention_sm_b200.build`)")
+    spec = importlib.util.spec_from_file_location("_paged_calls", CALLS)
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     lib = load()
