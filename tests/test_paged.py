@@ -1072,3 +1072,213 @@ def test_the_library_is_built_before_the_compiled_calls(monkeypatch):
     monkeypatch.setattr(build, "build_library", lambda *a: order.append("library"))
     monkeypatch.setattr(build, "build_calls", lambda *a: order.append("calls"))
     assert build.build() == build.LIB and order == ["library", "calls"]
+
+
+# ---- one page per sequence: the decode step's caches -----------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page,new,kv", [
+    (333, [70, 1, 20], [333, 1, 300]), (13, [13, 5], [13, 13]), (1, [1, 1], [1, 1]),
+    (200, [1, 1], [200, 129]), (2500, [40, 300], [2500, 2000]), (64, [64], [64]),
+    (129, [33, 4], [129, 128]), (7, [1, 1], [7, 3]),
+])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 3)])
+def test_attn_one_page_per_sequence(lib, dtype, d, page, new, kv, window, sinks):
+    x = _batch(new, kv, 8, 2, d, page, dtype, seed=page, extra_cols=0)
+    assert x["args"][3].shape[1] == 1
+    _assert_attn(x, sd.paged_attn(*x["args"], window=window, sinks=sinks, max_new=max(new)),
+                 window, sinks)
+    _assert_attn(x, sd.paged_attn(*x["args"], window=window, sinks=sinks), window, sinks)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("ncap", [90, 333])
+def test_prefill_of_the_decode_steps_caches(lib, dtype, ncap):
+    """Prompts in two chunks and a token through plan, append and attention on
+    dense caches, which the decode step then reads."""
+    B, Hq, Hkv, d = 2, 8, 2, 64
+    g = torch.Generator().manual_seed(ncap)
+    K = torch.full((B, Hkv, ncap, d), float("nan"), dtype=dtype, device="cuda")
+    V = K.clone()
+    table, lens = _i32([[-1], [-1]]), _i32([0, 0])
+    free, count = _i32([1, 0]), _i32([2])  # sequence b gets page b
+    hist = [(torch.zeros(Hkv, 0, d, dtype=dtype),) * 2 for _ in range(B)]
+    total = [0, 0]
+    for new in ([50, 30], [33, 53], [1, 1]):
+        T = sum(new)
+        q, k, v = (torch.randn(T, h, d, generator=g).to(dtype) for h in (Hq, Hkv, Hkv))
+        p = sd.paged_plan(_i32(new), lens, table, free, count, ncap, T, B, kv_lens=lens,
+                          free_left=count)
+        assert table.tolist() == [[0], [1]]
+        sd.paged_append(K, V, k.cuda(), v.cuda(), p["slots"])
+        got = sd.paged_attn(q.cuda(), K, V, table, p["q_start"], lens, max_new=max(new))
+        starts = p["q_start"].tolist()
+        for b in range(B):
+            r = slice(starts[b], starts[b + 1])
+            hist[b] = (torch.cat([hist[b][0], k[r].transpose(0, 1)], 1),
+                       torch.cat([hist[b][1], v[r].transpose(0, 1)], 1))
+            total[b] += new[b]
+            assert torch.equal(K[b, :, :total[b]].cpu(), hist[b][0])
+            assert torch.equal(V[b, :, :total[b]].cpu(), hist[b][1])
+        x = dict(new=new, kv=total, starts=starts, dense=hist, q=q, Hq=Hq, Hkv=Hkv, d=d,
+                 dtype=dtype)
+        _assert_attn(x, got)
+    n = total[0]
+    assert total == [n, n] and torch.isnan(K[:, :, n:]).all()
+    K[:, :, n:], V[:, :, n:] = 0, 0
+    step = sd.decode_step(q.cuda(), q.cuda()[None], K, V, k=n, n=n)
+    tol = 2.0 ** -5 if dtype == BF16 else 1e-5
+    assert (step["out"][0].float() - got[0].float()).abs().max() <= tol
+    assert (step["lse"][0] - got[1]).abs().max() <= 1e-3
+
+
+# ---- heads, pages ------------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("G", range(1, 17))
+def test_attn_chunks_of_every_group_size(lib, dtype, G):
+    x = _batch([40, 300, 1], [200, 300, 77], 2 * G, 2, 64, 16, dtype, seed=G)
+    _assert_attn(x, sd.paged_attn(*x["args"]))
+    _assert_attn(x, sd.paged_attn(*x["args"], window=90, sinks=70), 90, 70)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("page", [16, 48, 80, 96, 128, 144, 256, 400])
+def test_attn_chunks_of_every_page_size(lib, dtype, page):
+    x = _batch([60, 5, 300], [700, 5, 401], 8, 2, 128, page, dtype, seed=page)
+    _assert_attn(x, sd.paged_attn(*x["args"]))
+    _assert_attn(x, sd.paged_attn(*x["args"], window=150, sinks=20), 150, 20)
+
+
+# ---- weights in two parts ------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hkv,n", [(1, 100), (8, 64), (2, 33)])
+def test_attn_decode_keeps_16_bits_of_the_weights(lib, d, Hkv, n):
+    """Values whose weighted sum almost cancels show the rounding of the
+    weights.  q and k are small whole numbers, so scores are exact before they
+    are scaled.  With w the weights and A = sum_j w_j |v_j|: scaled scores and
+    their exponential are off by less than 2^-20 relative, sums over n keys by
+    4 n 2^-24 (products that are cut, not rounded), a weight in two bf16 parts
+    by 2^-16, the result by 2^-8 of itself."""
+    g = torch.Generator().manual_seed(n + d)
+    x = _batch([1], [n], Hkv, Hkv, d, 16, BF16, seed=n)
+    q, K, V, table = x["args"][:4]
+    qi = torch.randint(-1, 2, (1, Hkv, d), generator=g).to(BF16)
+    ki = torch.randint(-1, 2, (Hkv, n, d), generator=g).to(BF16)
+    z = torch.einsum("hd,hjd->hj", qi[0].double(), ki.double()) / math.sqrt(d)
+    w = torch.softmax(z, -1)
+    v = torch.randn(Hkv, n, d, generator=g).double()
+    v = (v - torch.einsum("hj,hjd->hd", w, v)[:, None]).to(BF16)
+    q.copy_(qi)
+    for j in range(0, n, 16):
+        m = min(16, n - j)
+        K[table[0, j // 16], :, :m] = ki[:, j:j + m].cuda()
+        V[table[0, j // 16], :, :m] = v[:, j:j + m].cuda()
+    want = torch.einsum("hj,hjd->hd", w, v.double())
+    A = torch.einsum("hj,hjd->hd", w, v.double().abs())
+    tol = (2.0 ** -20 + 4 * n * 2.0 ** -24 + 2.0 ** -16) * A + 2.0 ** -8 * want.abs()
+    got = sd.paged_attn(*x["args"], max_new=1)[0][0].double().cpu()
+    assert ((got - want).abs() / tol).max() <= 1
+    # one bf16 part alone would be far outside
+    p = torch.exp(z - z.amax(-1, keepdim=True))
+    one = torch.einsum("hj,hjd->hd", p.to(BF16).double(), v.double()) / p.sum(-1, keepdim=True)
+    assert ((one - want).abs() / tol).max() > 4
+
+
+# ---- graphs and streams that overlap ---------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_captured_chunks_follow_the_lengths(lib, dtype):
+    """One captured step of up to 40 new tokens per sequence, replayed with
+    other lengths: the schedule, the claim counter and the pieces of long
+    ranges are made anew each time, in two graphs in turn."""
+    B, Hq, Hkv, d, page, T = 2, 8, 1, 64, 16, 64
+    g = torch.Generator().manual_seed(6)
+    x = _batch([1] * B, [5000, 100], Hq, Hkv, d, page, dtype, seed=2, extra_cols=20)
+    _, K0, V0, table, _, _ = x["args"]
+    used, pages = K0.shape[0], K0.shape[0] + 40
+    K = torch.full((pages, Hkv, page, d), float("nan"), dtype=dtype, device="cuda")
+    V = K.clone()
+    K[:used], V[:used] = K0, V0
+    free = torch.arange(used, pages, dtype=torch.int32, device="cuda")
+    count, lens, new = _i32([pages - used]), _i32([5000, 100]), _i32([1, 1])
+    q = torch.zeros(T, Hq, d, dtype=dtype, device="cuda")
+    k = torch.zeros(T, Hkv, d, dtype=dtype, device="cuda")
+    v = torch.zeros_like(k)
+    graphs, outs, starts = [], [], []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            p = sd.paged_plan(new, lens, table, free, count, page, T, pages, check=False,
+                              kv_lens=lens, free_left=count)
+            sd.paged_append(K, V, k, v, p["slots"], check=False)
+            outs.append(sd.paged_attn(q, K, V, table, p["q_start"], lens, max_new=40,
+                                      check=False))
+        graphs.append(gr)
+        starts.append(p["q_start"])
+    hist, total = x["dense"], [5000, 100]
+    for step, ns in enumerate(([40, 3], [1, 40], [0, 17], [30, 0], [1, 1], [39, 25])):
+        n = sum(ns)
+        qn = torch.randn(n, Hq, d, generator=g).to(dtype)
+        kn, vn = (torch.randn(n, Hkv, d, generator=g).to(dtype) for _ in range(2))
+        new.copy_(_i32(ns)), q[:n].copy_(qn), k[:n].copy_(kn), v[:n].copy_(vn)
+        for o in outs[step % 2]:
+            o.fill_(7)
+        graphs[step % 2].replay()
+        at = starts[step % 2].tolist()
+        assert at == [0, ns[0], n]
+        hist = [tuple(torch.cat([old, t[at[b]:at[b + 1]].transpose(0, 1)], 1)
+                      for old, t in zip(hist[b], (kn, vn))) for b in range(B)]
+        total = [c + m for c, m in zip(total, ns)]
+        y = dict(new=ns, kv=total, starts=at, dense=hist, q=qn, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype)
+        _assert_attn(y, outs[step % 2])
+        assert all((o[n:] == 7).all() for o in outs[step % 2])
+    assert sd.paged_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_calls_that_overlap_keep_their_scratch_apart(lib, captured, dtype, new):
+    """Calls whose ranges are cut for all SMs, on two streams (or in two graphs
+    replayed there) with no order between them."""
+    xs = [_batch([new], [20000], 8, 2, 128, 16, dtype, seed=7),
+          _batch([new, new], [9000, 7000], 4, 1, 128, 16, dtype, seed=8)]
+    alone = [sd.paged_attn(*x["args"], max_new=new) for x in xs]
+    for x, a in zip(xs, alone):
+        _assert_attn(x, a)
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    calls = [lambda x=x: sd.paged_attn(*x["args"], max_new=new, check=False) for x in xs]
+    if captured:
+        graphs = [torch.cuda.CUDAGraph() for _ in xs]
+        outs = []
+        for gr, f in zip(graphs, calls):
+            with torch.cuda.graph(gr):
+                outs.append(f())
+        def replay(i):
+            graphs[i].replay()
+            return tuple(o.clone() for o in outs[i])
+        calls = [lambda: replay(0), lambda: replay(1)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(25):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(calls[i]())
+    torch.cuda.synchronize()
+    for a, each in zip(alone, got):
+        for o in each:
+            assert torch.equal(o[0], a[0]) and torch.equal(o[1], a[1])
+    for s in streams:
+        with torch.cuda.stream(s):
+            assert sd.paged_status() == 0
