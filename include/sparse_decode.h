@@ -384,7 +384,7 @@ typedef struct {
   int32_t page_size;  /* tokens per page */
   int32_t num_pages;  /* pages in K and in V */
   int32_t max_blocks; /* columns of the block table */
-  int32_t max_new;    /* most new tokens that one sequence has (0: T) */
+  int32_t max_new;    /* most new tokens that one sequence has (0: T); picks the kernels */
 } sparse_paged_shape_t;
 
 /* Bytes of workspace that sparse_paged_attn needs for this shape (the other
@@ -424,7 +424,8 @@ sparse_status_t sparse_paged_plan(const sparse_paged_shape_t *shape, const int32
  * [Hkv,d], k_stride and v_stride elements apart) becomes row slots[t] %
  * page_size of page slots[t] / page_size in K and V, for every head.  Rows
  * with slot -1 are skipped; other slots outside the pool are skipped and
- * raise SPARSE_ERR_INDEX in the device status.  Slots are distinct. */
+ * raise SPARSE_ERR_INDEX in the device status.  Slots are distinct, and no row
+ * that the call writes is one that it reads. */
 sparse_status_t sparse_paged_append(const sparse_paged_shape_t *shape, void *K, void *V,
                                     const void *k_new, int64_t k_stride, const void *v_new,
                                     int64_t v_stride, const int32_t *slots, void *ws,
@@ -436,7 +437,14 @@ sparse_status_t sparse_paged_append(const sparse_paged_shape_t *shape, void *K, 
  * only those with j > p - window or j < sinks.  out [T,Hq,d], lse [T,Hq] or
  * NULL, as in sparse_attn_gather (nothing seen: o = 0, lse = -inf); padding
  * rows are left as they were.  K and V already hold the new tokens' rows.
- * out and lse overlap neither each other nor q, K or V (refused).
+ * out and lse overlap neither each other nor q, K or V (refused), nor the
+ * other arguments.
+ * max_new picks the kernels.  Up to 16 rows per KV head (max_new * Hq / Hkv)
+ * every cache row is read once at the memory's rate, and bf16 weights keep 16
+ * bits; above, the rows go through blocks of 128 or 256, and bf16 weights are
+ * rounded to bf16 once (error of out against fp64 0.0022-0.0024 relative, of its
+ * own rounding alone 0.0017).  So a batch of single tokens should say
+ * max_new = 1: left at 0 it stands for T, and the batch takes the blocks.
  * A page id outside [0, num_pages) hides its tokens and raises
  * SPARSE_ERR_INDEX; a sequence with lengths outside the shape (rows outside
  * [0,T], more than max_new new tokens, a negative kv_len or one beyond its

@@ -23,16 +23,20 @@
 // at d = 128).  M = 128, N = 64 reads 6 KB of shared memory for 32 cycles of
 // products, 48 cycles; S tiles of 128 keys, one buffer each, need 64 for 64 but
 // make every row tile one chain, scores - softmax - product - scores: 888 TFLOP/s
-// against 1,107 (1,135 now; a 2,048-token chunk of 32K, 32 query heads over 8, d = 128).
+// against 1,107 (a 2,048-token chunk of 32K, 32 query heads over 8, d = 128; now
+// 1,100-1,130 in short runs at 1,965 MHz, 980-1,000 once the power cap has brought
+// the clock to 1,710-1,750 MHz).  Its 256 items on 148 SMs leave 13 % of them idle.
 // Handing P over in two halves costs more in the softmax than the earlier
 // product gains (921).
 //
 // The reference m of a row is only raised when the running maximum has left it
 // by more than 2^8: weights then reach 256 instead of 1, the sums stay fp32,
 // the division at the end cancels m, and O is almost never rescaled.
-// P is rounded to bf16 (2^-9 of each weight on average, independent errors
-// that the sum over keys averages; the result is rounded to bf16 anyway); its
-// sum is taken before the rounding.
+// P is rounded to bf16 once, where the decode kernel keeps two parts: a second
+// product per tile would lengthen the unit that bounds this kernel by 40 %.
+// Its sum is taken before the rounding.  The errors of single weights are
+// independent and about as large as the rounding of the result, so the result
+// is off by 0.0022-0.0024 of its norm where that rounding alone makes 0.0017.
 //
 // Every wait is bounded; when one runs out the kernel raises TIMEOUT, all
 // roles leave their loops, each waits for what it still has in flight (copies,

@@ -7,8 +7,8 @@
 // which costs little where memory is the limit.
 //
 // Measured: 16 ragged sequences of up to 65,536 tokens over 8 KV heads at
-// d = 128, 379-384 us, 6.9 TB/s of K and V (the copy rate, reads and writes, is
-// 6.6); one sequence of 131,072 tokens, 88 us.
+// d = 128, 380-390 us, 6.8-6.9 TB/s of K and V (the copy rate, reads and writes,
+// is 6.6); one sequence of 131,072 tokens, 88-90 us.
 #include "paged_decode.cuh"
 
 namespace sd {

@@ -13,7 +13,7 @@ A serving step is ``paged_plan`` once, then per layer ``paged_append`` and
 
     p = sd.paged_plan(new_lens, lens, table, free_pages, free_count, 64, T, num_pages)
     sd.paged_append(K, V, k_new, v_new, p["slots"])
-    out, lse = sd.paged_attn(q, K, V, table, p["q_start"], p["kv_lens"])
+    out, lse = sd.paged_attn(q, K, V, table, p["q_start"], p["kv_lens"], max_new=n)
     lens, free_count = p["kv_lens"], p["free_left"]
 
 Without ``ws`` a call uses a workspace kept for its device and stream, which
@@ -338,8 +338,8 @@ def paged_plan(new_lens, lens, block_table, free_pages, free_count, page_size: i
 def paged_append(K, V, k_new, v_new, slots, ws: Workspace | None = None, check: bool = True):
     """Write the new tokens' rows k_new, v_new [T,Hkv,d] (column ranges of
     wider rows are fine) to their slots [T] int32 of the paged caches K, V
-    [num_pages,Hkv,page_size,d]; rows with slot -1 are skipped, and the other
-    slots are distinct."""
+    [num_pages,Hkv,page_size,d]; rows with slot -1 are skipped, the other slots
+    are distinct, and no row is both read and written."""
     if ws is None:
         plain = _plain(K)
         if plain is not None:
@@ -377,8 +377,10 @@ def paged_attn(q, K, V, block_table, q_start, kv_lens, window: int = 0, sinks: i
     q_start[b+1] - 1 (q_start [B+1], kv_lens [B] int32: what paged_plan
     returned); row i stands at position p = kv_lens[b] - new tokens + i and
     sees tokens j <= p, under ``window`` >= 1 only those with j > p - window
-    or j < ``sinks``.  max_new: the most new tokens one sequence has, if known
-    (1 for a decode step: the kernels for few rows need it).  Returns
+    or j < ``sinks``.  max_new: the most new tokens one sequence has (1 for a
+    decode step).  Up to 16 rows per KV head, max_new * Hq / Hkv, take the kernels
+    for few rows, which are faster there and keep 16 bits of a bf16 call's
+    weights (8 in the others); left out, it stands for T.  Returns
     (out [T,Hq,d], lse [T,Hq] or None); rows behind the last sequence are not
     written.  ``out`` and ``lse`` overlap no other tensor of the call."""
     if ws is None:
