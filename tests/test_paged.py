@@ -11,6 +11,7 @@ Z = max_j sum_i |q_i k_ji| / sqrt(d):
 * bf16 kernels may round a weight to bf16 (2^-8 A) and round the result once
   (2^-8 |o|)."""
 import ctypes
+import gc
 import math
 import threading
 import time
@@ -955,6 +956,7 @@ def test_a_wait_that_ran_out_costs_the_kept_workspace(lib, checked):
 def test_kept_workspaces_can_be_freed(lib):
     x = _batch([300], [300], 8, 2, 128, 16, BF16)
     sd.paged_release()
+    gc.collect()
     torch.cuda.synchronize()
     before = torch.cuda.memory_allocated()
     got = sd.paged_attn(*x["args"])
@@ -963,6 +965,35 @@ def test_kept_workspaces_can_be_freed(lib):
     sd.paged_release()
     assert torch.cuda.memory_allocated() == before
     _assert_attn(x, sd.paged_attn(*x["args"]))
+
+
+def test_status_is_not_read_inside_a_capture(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: True)
+    with pytest.raises(ValueError, match="capture"):
+        sd.paged_status()
+
+
+@pytest.mark.parametrize("own,static,rc,left", [(0, 0, 0, 1), (0, 8, 8, 1), (4, 0, 4, 1),
+                                                (7, 8, 7, 0), (8, 7, 8, 1), (7, 0, 7, 0)])
+def test_status_of_both_words_is_read(monkeypatch, own, static, rc, left):
+    from token_sparse_attention_sm_b200 import paged
+    ws = sd.Workspace("cpu")
+    ws.key = (0, 5)
+    ws.get(4096)
+    reads = {ws.buf.data_ptr(): own, 4096: static}
+    class Library:
+        @staticmethod
+        def sparse_read_device_status(at, stream, flags):
+            assert stream == 5
+            return reads.pop(at)
+    monkeypatch.setattr(paged, "_stream_ws", {(0, 5): ws})
+    monkeypatch.setattr(paged, "load", lambda: Library)
+    monkeypatch.setattr(paged, "_static_status", lambda dev: 4096)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 5)
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False)
+    assert sd.paged_status(raise_on_error=False) == rc
+    assert not reads and len(paged._stream_ws) == left
 
 
 def test_only_a_wait_that_ran_out_costs_the_kept_workspace(monkeypatch):

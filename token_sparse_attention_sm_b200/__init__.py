@@ -239,9 +239,9 @@ def workspace_bytes(B, N, Hq, Hkv, d, dtype, k_or_cap: int, L: int) -> int:
 class Workspace:
     """A zero-initialised device workspace that grows on demand.  Calls that
     share one must be ordered on the same stream.  Growing replaces the
-    buffer (the status word goes along): a CUDA graph captured earlier keeps using the old one, so whoever
-    holds such a graph also holds a reference to the buffer it captured
-    (DecodeStepGraph does)."""
+    buffer (the status word goes along): a CUDA graph captured earlier keeps
+    using the old one, so whoever holds such a graph also holds a reference to
+    the buffer it captured (DecodeStepGraph does)."""
 
     def __init__(self, device=None):
         self.device = torch.device(device) if device is not None else torch.device(

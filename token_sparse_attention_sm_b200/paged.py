@@ -210,18 +210,23 @@ def _static_status(dev: int) -> int:
 
 def paged_status(raise_on_error: bool = True) -> int:
     """Synchronise the current stream and read (and reset) the device status of
-    the paged calls made without ``ws``: those on this stream, and those that
-    any graph captured on this device has replayed up to now.  Raises
-    SparseDecodeError unless it is SPARSE_OK; else returns it."""
+    the paged calls made without ``ws``: those on this stream, and those captured
+    on this device, whose replays should be over (what one in flight reports may
+    be missed).  Raises SparseDecodeError unless it is SPARSE_OK; else returns it."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        raise ValueError("reading the status synchronises: not inside a stream capture")
     dev = torch.cuda.current_device()
     stream = torch._C._cuda_getCurrentRawStream(dev)
     ws = _stream_ws.get((dev, stream))
     rc, seen = 0, 0
-    for at in ([] if ws is None else [ws.buf.data_ptr()]) + [_static_status(dev)]:
+    words = [(None, _static_status(dev))]
+    if ws is not None:
+        words.append((ws, ws.buf.data_ptr()))
+    for w, at in words:
         flags = ctypes.c_uint32(0)
-        rc = load().sparse_read_device_status(at, stream, ctypes.byref(flags)) or rc
-        seen |= flags.value
-    _drop_after(rc, ws)
+        one = load().sparse_read_device_status(at, stream, ctypes.byref(flags))
+        _drop_after(one, w)
+        rc, seen = one or rc, seen | flags.value
     if raise_on_error:
         _check(rc, f"device status (flags=0x{seen:x})")
     return rc
