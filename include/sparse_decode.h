@@ -455,7 +455,9 @@ sparse_status_t sparse_paged_append(const sparse_paged_shape_t *shape, void *K, 
  * NaN or +inf (from q or a visible row of K) is NaN, and so is its lse; the
  * other rows are not touched by it.  (In fp32 with more than 16 rows per KV
  * head, max_new * Hq / Hkv, an infinite element of q or K makes every score it
- * enters NaN.) */
+ * enters NaN.)  Sums are fp32 over weights of up to 2^8 (a row's reference
+ * follows its maximum late), so 256 times the sum of a column's |V| over the
+ * tokens a row sees should stay below fp32's largest number. */
 sparse_status_t sparse_paged_attn(const sparse_paged_shape_t *shape, const void *q,
                                   int64_t q_stride, const void *K, const void *V,
                                   const int32_t *block_table, const int32_t *q_start,
